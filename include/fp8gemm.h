@@ -229,6 +229,92 @@ fg_status fp8_cast_blocks(const void* X, void* Q, float* sfb, int G, int N, int 
 fg_status fp8_cast_rows_ex(const void* X, void* Q, float* sfa, int G, int M, int K, int fmt, void* stream);
 fg_status fp8_cast_blocks_ex(const void* X, void* Q, float* sfb, int G, int N, int K, int fmt, void* stream);
 
+/* ------------------------------------------------------------------ around the GEMMs
+ * The operators between a layer's tokens and the grouped GEMMs, and low-rank adapters beside
+ * a projection.  All pointers are device pointers owned by the caller; nothing is allocated, no
+ * call needs fg_init, and every call can be captured into a CUDA graph.  `scratch` is device
+ * memory of at least the stated size with any contents, needed until the call's kernels have
+ * run; calls that may run at the same time need different scratch.  Results are deterministic.
+ * Value types of the router's logits: */
+typedef enum { FG_F32 = 0, FG_BF16 = 1, FG_F16 = 2 } fg_dtype;
+#define FG_MOE_MAX_EXPERTS 1024
+
+/* The router: top-k choice, weights, per-expert counts and balance loss of S sequences of T
+ * tokens.  logits [S][T][E] of type `dtype`; mask [S][T] bytes, 0 = a token that is not routed
+ * (its logits may hold anything), NULL = every token.  Per routed token, with p = softmax of
+ * its logits over all E: ids [S][T][k] int32 are the k largest logits, largest first, the lowest
+ * expert first among equals; weights [S][T][k] are p at the ids, divided by their sum when
+ * `renormalize`.  A logit of -inf or NaN is never chosen: choices that are left over have id -1
+ * and weight 0, and a token without any choice is not routed.  (NaN and +inf logits of a routed
+ * token still make its weights and the loss NaN, as the softmax does.)  Per sequence, over its n
+ * routed tokens: counts [S][E], the choices of each expert; with f = counts / sum(counts) and P
+ * the mean of p: loss [S] = E * sum_e f_e P_e (1 for an even load; 0 with n = 0) and
+ * slope [S][E] = E f_e / n, the derivative of the loss by each token's p (counts are not
+ * differentiated), for the backward pass.  Sums are fp32.  1 <= k <= min(E, 32),
+ * E <= FG_MOE_MAX_EXPERTS, S <= 65535, else FG_ERR_UNSUPPORTED (k > E: FG_ERR_INVALID_ARG).
+ * T = 0 gives zero counts, loss and slope; S = 0 is a no-op. */
+size_t fg_moe_route_scratch_bytes(int S, int T, int E);
+fg_status fg_moe_route(const void* logits, int dtype, const unsigned char* mask, int* ids, float* weights,
+                       int* counts, float* loss, float* slope, int S, int T, int E, int k, int renormalize,
+                       void* scratch, size_t scratch_bytes, void* stream);
+
+/* Gradient of the router: grad_logits [S][T][E] (type of the logits, rounded once from fp32) from
+ * grad_weights [S][T][k] and grad_loss [S], either NULL for none, with the ids and slope of the
+ * forward call.  Tokens that were not routed (all ids -1) get zeros. */
+fg_status fg_moe_route_backward(const void* logits, int dtype, const int* ids, const float* slope,
+                                const float* grad_weights, const float* grad_loss, void* grad_logits, int S,
+                                int T, int E, int k, int renormalize, void* stream);
+
+/* The experts' row layout of `pairs` (token, choice) pairs: ids [pairs] is each pair's expert, any
+ * value outside [0, E) = none (an expert of another GPU, a choice left over).  rows [pairs] gets
+ * each pair's row, -1 for none; an expert's pairs take its rows in order.
+ * Contiguous: the experts' blocks one after the other, each padded to fg_m_alignment() rows;
+ *   m_indices [M] as fp8_gemm_grouped_contiguous reads it (-1 = padding, and everything behind
+ *   the last block).  M is at least fg_moe_layout_rows(pairs, E), the most rows that any choice
+ *   takes, so that the host need not know the counts.
+ * Masked: expert e has rows e * mmax .. e * mmax + mmax - 1; pairs beyond mmax get row -1 and
+ *   masked_m [E] = min(count, mmax).
+ * E <= FG_MOE_MAX_EXPERTS, pairs <= 2^24, E * mmax < 2^31, else FG_ERR_UNSUPPORTED. */
+long long fg_moe_layout_rows(long long pairs, int E);
+size_t fg_moe_layout_scratch_bytes(long long pairs, int E);
+fg_status fg_moe_layout_contiguous(const int* ids, int* rows, int* m_indices, long long pairs, int E, int M,
+                                   void* scratch, size_t scratch_bytes, void* stream);
+fg_status fg_moe_layout_masked(const int* ids, int* rows, int* masked_m, long long pairs, int E, int mmax,
+                               void* scratch, size_t scratch_bytes, void* stream);
+
+/* Cast the tokens' rows into the layout: for each token t and each row r = rows[t][j] in [0, G * M),
+ * the codes and scales of x[t] (exactly those of fp8_cast_rows_ex) are stored at row r.
+ * x bf16 [T][K], rows [T][k]; A [G][M][K] codes and sfa [G][ceil(K/128)][fg_sfa_ld(M)]:
+ * G = 1 and M = all rows for the contiguous layout, G = E and M = mmax for the masked one.  Rows
+ * that no pair has keep their contents.  No row may stand in `rows` twice (rows of
+ * fg_moe_layout_* never do).  K % 16 == 0, k <= 32, G * M < 2^31; x must be finite. */
+fg_status fg_moe_dispatch_fp8(const void* x, const int* rows, void* A, float* sfa, int T, int k, int G, int M,
+                              int K, int fmt, void* stream);
+
+/* out[t] = sum_j weights[t][j] * C[rows[t][j]] over the pairs with a row in [0, M), summed in fp32 in
+ * the order of j and rounded once to bf16; weights NULL = all 1 (the gradient of the dispatch).  C bf16
+ * [M][N], out bf16 [T][N], which must not overlap C.  A token without rows gets zeros.  N % 8 == 0,
+ * k <= 32. */
+fg_status fg_moe_combine(const void* C, const int* rows, const float* weights, void* out, int T, int k, int M,
+                         int N, void* stream);
+
+/* Gradients of fg_moe_combine: grad_C[rows[t][j]] = bf16(weights[t][j] * grad_out[t]) (the other
+ * rows of grad_C keep their contents) and grad_weights[t][j] = <grad_out[t], C[rows[t][j]]> in fp32, 0
+ * for a pair without a row.  No row may stand in `rows` twice; grad_C must not overlap C or
+ * grad_out. */
+fg_status fg_moe_combine_backward(const void* grad_out, const void* C, const int* rows, const float* weights,
+                                  void* grad_C, float* grad_weights, int T, int k, int M, int N, void* stream);
+
+/* Low-rank adapters beside a projection: out[m] = C[m] + scaling[a] * B_a (A_a x[m]), a =
+ * adapters[m] in [0, L); any other value leaves out[m] = C[m].  C, out bf16 [M][N] (out may be C),
+ * x bf16 [M][K], lora_a bf16 [L][R][K], lora_b bf16 [L][N][R], scaling fp32 [L] or NULL (all 1).
+ * Both products accumulate in fp32, A_a x is kept to 16 bits of mantissa between them, and the sum
+ * is rounded once.  K % 16 == 0, N % 8 == 0, R % 8 == 0, R <= 128 (a smaller rank is padded with
+ * zeros).  Rows of one adapter may stand anywhere. */
+fg_status fg_lora_add(const void* C, const void* x, const void* lora_a, const void* lora_b,
+                      const int* adapters, const float* scaling, void* out, int M, int N, int K, int R, int L,
+                      void* stream);
+
 /* Synchronise `stream`, then read and clear the device status word:
  * FG_OK, or FG_ERR_TIMEOUT if some kernel since the last call gave up a wait, or (debug
  * build, libfp8gemm_debug.so, compiled with -DFG_DEBUG) FG_ERR_DEVICE_CHECK if a

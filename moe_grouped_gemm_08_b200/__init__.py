@@ -12,6 +12,8 @@ Entry points (names after the DeepGEMM how-to, aisharenet.com, "Main functions")
 Layouts: A [M,K] / [G,Mmax,K] e4m3 (uint8 or float8_e4m3fn); sfa fp32 column-major
 per K block, [KB, sfa_ld(M)] / [G, KB, sfa_ld(Mmax)]; B [N,K] / [G,N,K]; sfb fp32
 [NB, KB] / [G, NB, KB]; C bf16 [M,N] / [G,Mmax,N].  See include/fp8gemm.h.
+The operators around the GEMMs (moe_route, moe_layout_*, moe_dispatch_fp8, moe_combine, lora_add and
+the gradients) are in operators.py and importable from here.
 """
 from __future__ import annotations
 
@@ -105,6 +107,28 @@ def _declare(l: ctypes.CDLL) -> ctypes.CDLL:
     l.fp8_gemm_grouped_masked_ws.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _int, _int, _int, _int, _int, _int,
                                              ctypes.c_uint, _vp, ctypes.c_size_t, _vp]
     l.fp8_gemm_grouped_masked_ws.restype = _int
+    l.fg_moe_route_scratch_bytes.argtypes = [_int, _int, _int]
+    l.fg_moe_route_scratch_bytes.restype = ctypes.c_size_t
+    l.fg_moe_route.argtypes = [_vp, _int, _vp, _vp, _vp, _vp, _vp, _vp, _int, _int, _int, _int, _int, _vp,
+                               ctypes.c_size_t, _vp]
+    l.fg_moe_route.restype = _int
+    l.fg_moe_route_backward.argtypes = [_vp, _int, _vp, _vp, _vp, _vp, _vp, _int, _int, _int, _int, _int, _vp]
+    l.fg_moe_route_backward.restype = _int
+    l.fg_moe_layout_rows.argtypes = [ctypes.c_longlong, _int]
+    l.fg_moe_layout_rows.restype = ctypes.c_longlong
+    l.fg_moe_layout_scratch_bytes.argtypes = [ctypes.c_longlong, _int]
+    l.fg_moe_layout_scratch_bytes.restype = ctypes.c_size_t
+    for name in ("fg_moe_layout_contiguous", "fg_moe_layout_masked"):
+        getattr(l, name).argtypes = [_vp, _vp, _vp, ctypes.c_longlong, _int, _int, _vp, ctypes.c_size_t, _vp]
+        getattr(l, name).restype = _int
+    l.fg_moe_dispatch_fp8.argtypes = [_vp, _vp, _vp, _vp, _int, _int, _int, _int, _int, _int, _vp]
+    l.fg_moe_dispatch_fp8.restype = _int
+    l.fg_moe_combine.argtypes = [_vp, _vp, _vp, _vp, _int, _int, _int, _int, _vp]
+    l.fg_moe_combine.restype = _int
+    l.fg_moe_combine_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _int, _int, _int, _int, _vp]
+    l.fg_moe_combine_backward.restype = _int
+    l.fg_lora_add.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _int, _int, _int, _int, _int, _vp]
+    l.fg_lora_add.restype = _int
     l.fg_launch_count.argtypes = []
     l.fg_launch_count.restype = ctypes.c_uint64
     return l
@@ -437,3 +461,9 @@ def cast_fp8_blocks(w, stream=None, fmt="e4m3"):
         _check(_lib.fp8_cast_blocks_ex(w.data_ptr(), q.data_ptr(), sfb.data_ptr(), G, N, K, FORMATS[fmt],
                                        _stream(stream, w.device)), "fp8_cast_blocks")
     return q, (sfb if grouped else sfb[0])
+
+
+# ---------------------------------------------------------------------------- around the GEMMs
+from .operators import (  # noqa: E402
+    lora_add, moe_combine, moe_combine_backward, moe_dispatch_fp8, moe_layout_contiguous, moe_layout_masked,
+    moe_layout_rows, moe_route, moe_route_backward)

@@ -9,15 +9,19 @@ HERE = pathlib.Path(__file__).resolve().parent
 ROOT = HERE.parent
 SO = HERE / "libfp8gemm.so"
 SO_DEBUG = HERE / "libfp8gemm_debug.so"  # the same library with the device-side checks (-DFG_DEBUG)
-SOURCES = [HERE / "csrc" / "fp8gemm_api.cu"]
-DEPENDS = SOURCES + [HERE / "csrc" / "fp8_gemm_kernels.cuh", HERE / "csrc" / "fp8_cast_kernels.cuh",
-                     HERE / "csrc" / "sm100_ptx.cuh", HERE / "csrc" / "fp8gemm_jit.h",
-                     ROOT / "include" / "fp8gemm.h"]
+CSRC = HERE / "csrc"
+COMMON = [CSRC / "fp8_cast_kernels.cuh", CSRC / "sm100_ptx.cuh", ROOT / "include" / "fp8gemm.h"]
+# source -> what it includes
+SOURCES = {
+    CSRC / "fp8gemm_api.cu": COMMON + [CSRC / "fp8_gemm_kernels.cuh", CSRC / "fp8gemm_jit.h"],
+    CSRC / "operators_api.cu": COMMON + [CSRC / "moe_route_kernels.cuh", CSRC / "moe_rows_kernels.cuh",
+                                         CSRC / "lora_kernels.cuh"],
+}
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-shared", "-Xcompiler", "-fPIC", "-ldl",
+    "-Xcompiler", "-fPIC",
 ]
 
 
@@ -49,19 +53,34 @@ def write_jit_sources() -> pathlib.Path:
     return out
 
 
+def _newer(target: pathlib.Path, sources) -> bool:
+    return target.exists() and target.stat().st_mtime >= max(p.stat().st_mtime for p in sources)
+
+
 def _build_one(so: pathlib.Path, extra, force: bool, verbose: bool) -> pathlib.Path:
-    if not force and so.exists():
-        newest = max(p.stat().st_mtime for p in DEPENDS)
-        if so.stat().st_mtime >= newest:
-            return so
+    """Compile the sources that changed to objects (side by side) and link them to `so`."""
     write_jit_sources()
-    tmp = so.with_suffix(".so.tmp%d" % os.getpid())
-    cmd = [nvcc(), *NVCC_FLAGS, *extra, "-I", str(ROOT / "include"), "-I", str(HERE / "csrc"), "-I", str(GEN),
-           *(str(s) for s in SOURCES), "-o", str(tmp)]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.check_call(cmd)
-    os.replace(tmp, so)
+    objects, running = [], []
+    for src, includes in SOURCES.items():
+        obj = GEN / f"{so.stem}.{src.stem}.o"
+        objects.append(obj)
+        if not force and _newer(obj, [src, *includes, pathlib.Path(__file__)]):
+            continue
+        tmp = obj.with_suffix(".o.tmp%d" % os.getpid())
+        cmd = [nvcc(), *NVCC_FLAGS, *extra, "-I", str(ROOT / "include"), "-I", str(CSRC), "-I", str(GEN), "-c",
+               str(src), "-o", str(tmp)]
+        if verbose:
+            cmd.insert(1, "-Xptxas=-v")
+        running.append((subprocess.Popen(cmd), cmd, tmp, obj))
+    failed = [cmd for process, cmd, _, _ in running if process.wait() != 0]
+    if failed:
+        raise subprocess.CalledProcessError(1, failed[0])
+    for _, _, tmp, obj in running:
+        os.replace(tmp, obj)
+    if running or not _newer(so, objects):
+        tmp = so.with_suffix(".so.tmp%d" % os.getpid())
+        subprocess.check_call([nvcc(), *NVCC_FLAGS, "-shared", "-ldl", *(str(o) for o in objects), "-o", str(tmp)])
+        os.replace(tmp, so)
     return so
 
 

@@ -1,0 +1,420 @@
+// operators_api.cu -- host side of the operators around the GEMMs (the router, the experts' row
+// layout, dispatch, combine, low-rank adapters): argument checks and launches.  Nothing here
+// allocates, reads device memory or synchronises, so every call can be captured into a CUDA graph;
+// none needs fg_init.
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+#include <cstring>
+
+#include "fp8gemm.h"
+#include "lora_kernels.cuh"
+#include "moe_route_kernels.cuh"
+#include "moe_rows_kernels.cuh"
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int sm_count() {
+  static std::atomic<int> cached[kMaxDevices];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return 0;
+  }
+  int v = cached[dev].load(std::memory_order_relaxed);
+  if (v > 0) return v;
+  if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) {
+    cudaGetLastError();
+    return 0;
+  }
+  cached[dev].store(v, std::memory_order_relaxed);
+  return v;
+}
+
+// Programmatic dependent launch, as the GEMMs are launched: every kernel here waits for the preceding
+// grid before it touches global memory, and only then lets the next one start.
+template <typename... Params, typename... Args>
+fg_status launch(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, void* stream, int cluster,
+                 const Args&... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...) != cudaSuccess) {
+    cudaGetLastError();
+    return FG_ERR_CUDA;
+  }
+  return FG_OK;
+}
+
+// The opt-in shared-memory size of a kernel, set once per device (not again during a capture).
+template <auto KERNEL>
+bool allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  const uint64_t bit = 1ull << dev;
+  if (done.load(std::memory_order_acquire) & bit) return true;
+  if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  done.fetch_or(bit, std::memory_order_acq_rel);
+  return true;
+}
+
+long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
+
+// ------------------------------------------------------------------------------------ the router
+size_t value_bytes(int dtype) { return dtype == FG_F32 ? 4 : 2; }
+bool valid_dtype(int dtype) { return dtype == FG_F32 || dtype == FG_BF16 || dtype == FG_F16; }
+
+// Rows of a sequence per CTA: few enough that the SMs hold about four CTAs each, a multiple of the
+// rows that the warps of a CTA take at once (at most 32).
+int route_rows_per_chunk(int S, int T, int sms) {
+  long long rows = cdiv(static_cast<long long>(S) * T, 4ll * sms);
+  rows = cdiv(rows, 32) * 32;
+  return static_cast<int>(rows < T ? rows : T);
+}
+
+template <typename T, int LPR, int NPL, int V>
+fg_status route_launch(const fg::RouteParams& p, int S, void* stream) {
+  return launch(fg::moe_route_kernel<T, LPR, NPL, V>, dim3(p.chunks, S), fg::kRouteThreads, 0, stream, 1, p);
+}
+template <typename T, int LPR, int NPL, int V>
+fg_status route_launch(const fg::RouteGradParams& p, int S, void* stream) {
+  return launch(fg::moe_route_backward_kernel<T, LPR, NPL, V>, dim3(static_cast<unsigned>(cdiv(p.T, p.rows_per_chunk)), S),
+                fg::kRouteThreads, 0, stream, 1, p);
+}
+
+// The instance that holds E columns: few lanes a row for few experts, 16-byte loads where each row
+// starts on a 16-byte boundary.
+template <typename T, typename P>
+fg_status route_pick(const P& p, int S, bool wide, void* stream) {
+  constexpr int V = 16 / static_cast<int>(sizeof(T));
+  const int E = p.E;
+  if (wide) {
+    if (E <= 64) return route_launch<T, 8, 8, V>(p, S, stream);
+    if (E <= 128) return route_launch<T, 16, 8, V>(p, S, stream);
+    if (E <= 256) return route_launch<T, 32, 8, V>(p, S, stream);
+    if (E <= 512) return route_launch<T, 32, 16, V>(p, S, stream);
+    return route_launch<T, 32, 32, V>(p, S, stream);
+  }
+  if (E <= 8) return route_launch<T, 8, 1, 1>(p, S, stream);
+  if (E <= 32) return route_launch<T, 8, 4, 1>(p, S, stream);
+  if (E <= 64) return route_launch<T, 8, 8, 1>(p, S, stream);
+  if (E <= 128) return route_launch<T, 16, 8, 1>(p, S, stream);
+  if (E <= 256) return route_launch<T, 32, 8, 1>(p, S, stream);
+  if (E <= 512) return route_launch<T, 32, 16, 1>(p, S, stream);
+  return route_launch<T, 32, 32, 1>(p, S, stream);
+}
+
+template <typename P>
+fg_status route_dispatch(const P& p, int S, int dtype, bool wide, void* stream) {
+  if (dtype == FG_F32) return route_pick<float>(p, S, wide, stream);
+  if (dtype == FG_BF16) return route_pick<__nv_bfloat16>(p, S, wide, stream);
+  return route_pick<__half>(p, S, wide, stream);
+}
+
+fg_status route_check(int dtype, int S, int T, int E, int k) {
+  if (!valid_dtype(dtype) || S < 0 || T < 0 || E <= 0 || k <= 0 || k > E) return FG_ERR_INVALID_ARG;
+  if (E > FG_MOE_MAX_EXPERTS || k > fg::kRouteMaxK || S > 65535) return FG_ERR_UNSUPPORTED;
+  return FG_OK;
+}
+
+struct RouteScratch {
+  int chunks, rows;
+  size_t p_bytes, bytes;
+};
+RouteScratch route_scratch(int S, int T, int E, int sms) {
+  RouteScratch r;
+  r.rows = T > 0 ? route_rows_per_chunk(S, T, sms) : 1;
+  r.chunks = static_cast<int>(cdiv(T, r.rows));
+  r.p_bytes = static_cast<size_t>(S) * r.chunks * E * 4;
+  r.bytes = r.p_bytes + static_cast<size_t>(S) * r.chunks * (E + 1) * 4;
+  return r;
+}
+
+// ------------------------------------------------------------------------------------ row layouts
+int layout_chunks(long long pairs) { return static_cast<int>(cdiv(pairs, fg::kLayoutChunk)); }
+
+fg_status layout_run(const int* ids, int* rows, int* group, long long pairs, int E, int M, int mmax, void* scratch,
+                     size_t scratch_bytes, void* stream) {
+  fg::LayoutParams p;
+  p.ids = ids;
+  p.rows = rows;
+  p.group = group;
+  p.hist = static_cast<int*>(scratch);
+  p.pairs = pairs;
+  p.E = E;
+  p.chunks = layout_chunks(pairs);
+  p.M = M;
+  p.mmax = mmax;
+  p.align = fg_m_alignment();
+  if (p.chunks > 1) {
+    if (!scratch || scratch_bytes < fg_moe_layout_scratch_bytes(pairs, E)) return FG_ERR_INVALID_ARG;
+    if (!aligned(scratch, 4)) return FG_ERR_ALIGNMENT;
+    const fg_status s = launch(fg::moe_layout_count_kernel, dim3(p.chunks), fg::kLayoutThreads, 0, stream, 1, p);
+    if (s != FG_OK) return s;
+  }
+  return launch(fg::moe_layout_kernel, dim3(p.chunks > 0 ? p.chunks : 1), fg::kLayoutThreads, 0, stream, 1, p);
+}
+
+fg_status layout_check(const int* ids, const int* rows, const int* group, long long pairs, int E) {
+  if (pairs < 0 || E <= 0 || !group || (pairs > 0 && (!ids || !rows))) return FG_ERR_INVALID_ARG;
+  if (E > FG_MOE_MAX_EXPERTS || pairs > (1ll << 24)) return FG_ERR_UNSUPPORTED;
+  if (!aligned(ids, 4) || !aligned(rows, 4) || !aligned(group, 4)) return FG_ERR_ALIGNMENT;
+  return FG_OK;
+}
+
+template <int NT>
+fg_status lora_launch(const fg::LoraParams& p, void* stream) {
+  constexpr size_t smem = static_cast<size_t>(fg::kLoraWarps + 1) * 16 * NT * 8 * 4;
+  if (!allow_smem<fg::lora_rows_kernel<NT>>(smem)) return FG_ERR_CUDA;
+  return launch(fg::lora_rows_kernel<NT>, dim3(static_cast<unsigned>(p.M) * fg::kLoraCluster), fg::kLoraThreads, smem,
+                stream, fg::kLoraCluster, p);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fg_moe_route_scratch_bytes(int S, int T, int E) {
+  if (S <= 0 || T <= 0 || E <= 0) return 0;
+  const int sms = sm_count();
+  return sms > 0 ? route_scratch(S, T, E, sms).bytes : 0;
+}
+
+fg_status fg_moe_route(const void* logits, int dtype, const unsigned char* mask, int* ids, float* weights, int* counts,
+                       float* loss, float* slope, int S, int T, int E, int k, int renormalize, void* scratch,
+                       size_t scratch_bytes, void* stream) {
+  const fg_status bad = route_check(dtype, S, T, E, k);
+  if (bad != FG_OK) return bad;
+  if (S == 0) return FG_OK;
+  if (!counts || !loss || !slope || (T > 0 && (!logits || !ids || !weights || !scratch))) return FG_ERR_INVALID_ARG;
+  if (!aligned(logits, value_bytes(dtype)) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(counts, 4) ||
+      !aligned(loss, 4) || !aligned(slope, 4) || !aligned(scratch, 4))
+    return FG_ERR_ALIGNMENT;
+  const int sms = sm_count();
+  if (sms <= 0) return FG_ERR_CUDA;
+  const RouteScratch r = route_scratch(S, T, E, sms);
+  if (T > 0 && scratch_bytes < r.bytes) return FG_ERR_INVALID_ARG;
+  fg::RouteParams p;
+  p.logits = logits;
+  p.mask = mask;
+  p.ids = ids;
+  p.weights = weights;
+  p.counts = counts;
+  p.loss = loss;
+  p.slope = slope;
+  p.part_p = static_cast<float*>(scratch);
+  p.part_n = reinterpret_cast<int*>(static_cast<char*>(scratch) + r.p_bytes);
+  p.T = T;
+  p.E = E;
+  p.k = k;
+  p.chunks = r.chunks;
+  p.rows_per_chunk = r.rows;
+  p.renorm = renormalize ? 1 : 0;
+  if (T > 0) {
+    const size_t size = value_bytes(dtype);
+    const bool wide = aligned(logits, 16) && static_cast<size_t>(E) * size % 16 == 0;
+    const fg_status s = route_dispatch(p, S, dtype, wide, stream);
+    if (s != FG_OK) return s;
+  }
+  return launch(fg::moe_route_finish_kernel, dim3(S), static_cast<int>(cdiv(E, 32) * 32), 0, stream, 1, p);
+}
+
+fg_status fg_moe_route_backward(const void* logits, int dtype, const int* ids, const float* slope,
+                                const float* grad_weights, const float* grad_loss, void* grad_logits, int S, int T,
+                                int E, int k, int renormalize, void* stream) {
+  const fg_status bad = route_check(dtype, S, T, E, k);
+  if (bad != FG_OK) return bad;
+  if (S == 0 || T == 0) return FG_OK;
+  if (!logits || !ids || !slope || !grad_logits) return FG_ERR_INVALID_ARG;
+  const size_t size = value_bytes(dtype);
+  if (!aligned(logits, size) || !aligned(grad_logits, size) || !aligned(ids, 4) || !aligned(slope, 4) ||
+      !aligned(grad_weights, 4) || !aligned(grad_loss, 4))
+    return FG_ERR_ALIGNMENT;
+  const int sms = sm_count();
+  if (sms <= 0) return FG_ERR_CUDA;
+  fg::RouteGradParams p;
+  p.logits = logits;
+  p.ids = ids;
+  p.slope = slope;
+  p.grad_weights = grad_weights;
+  p.grad_loss = grad_loss;
+  p.grad_logits = grad_logits;
+  p.T = T;
+  p.E = E;
+  p.k = k;
+  p.rows_per_chunk = route_rows_per_chunk(S, T, sms);
+  p.renorm = renormalize ? 1 : 0;
+  const bool wide = aligned(logits, 16) && aligned(grad_logits, 16) && static_cast<size_t>(E) * size % 16 == 0;
+  return route_dispatch(p, S, dtype, wide, stream);
+}
+
+long long fg_moe_layout_rows(long long pairs, int E) {
+  if (pairs <= 0 || E <= 0) return 0;
+  const long long n = pairs < E ? pairs : E;  // experts with rows
+  return fg_m_alignment() * (n + (pairs - n) / fg_m_alignment());
+}
+
+size_t fg_moe_layout_scratch_bytes(long long pairs, int E) {
+  if (pairs <= fg::kLayoutChunk || E <= 0 || pairs > (1ll << 24)) return 0;
+  return static_cast<size_t>(layout_chunks(pairs)) * E * 4;
+}
+
+fg_status fg_moe_layout_contiguous(const int* ids, int* rows, int* m_indices, long long pairs, int E, int M,
+                                   void* scratch, size_t scratch_bytes, void* stream) {
+  if (pairs == 0 && M == 0 && E > 0) return FG_OK;
+  const fg_status s = layout_check(ids, rows, m_indices, pairs, E);
+  if (s != FG_OK) return s;
+  if (M < fg_moe_layout_rows(pairs, E)) return FG_ERR_INVALID_ARG;
+  return layout_run(ids, rows, m_indices, pairs, E, M, 0, scratch, scratch_bytes, stream);
+}
+
+fg_status fg_moe_layout_masked(const int* ids, int* rows, int* masked_m, long long pairs, int E, int mmax,
+                               void* scratch, size_t scratch_bytes, void* stream) {
+  const fg_status s = layout_check(ids, rows, masked_m, pairs, E);
+  if (s != FG_OK) return s;
+  if (mmax <= 0) return FG_ERR_INVALID_ARG;
+  if (static_cast<long long>(E) * mmax > 0x7fffffffll) return FG_ERR_UNSUPPORTED;
+  return layout_run(ids, rows, masked_m, pairs, E, 0, mmax, scratch, scratch_bytes, stream);
+}
+
+fg_status fg_moe_dispatch_fp8(const void* x, const int* rows, void* A, float* sfa, int T, int k, int G, int M, int K,
+                              int fmt, void* stream) {
+  if (T < 0 || k < 0 || G < 0 || M < 0 || K < 0 || (fmt != FG_E4M3 && fmt != FG_E5M2)) return FG_ERR_INVALID_ARG;
+  if (T == 0 || k == 0 || G == 0 || M == 0 || K == 0) return FG_OK;
+  if (!x || !rows || !A || !sfa) return FG_ERR_INVALID_ARG;
+  if (K % 16 != 0 || !aligned(x, 16) || !aligned(A, 16) || !aligned(sfa, 4) || !aligned(rows, 4))
+    return FG_ERR_ALIGNMENT;
+  if (k > fg::kRowsMaxK || static_cast<long long>(G) * M > 0x7fffffffll) return FG_ERR_UNSUPPORTED;
+  const int sms = sm_count();
+  if (sms <= 0) return FG_ERR_CUDA;
+  fg::DispatchParams p;
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.rows = rows;
+  p.A = static_cast<uint8_t*>(A);
+  p.sfa = sfa;
+  p.T = T;
+  p.k = k;
+  p.K = K;
+  p.M = G * M;
+  p.mmax = M;
+  p.ld = fg_sfa_ld(M);
+  const int chunks = static_cast<int>(cdiv(K, 256 * fg::kCastSpans));
+  long long blocks = cdiv(static_cast<long long>(T) * chunks, 8);
+  if (blocks > 8ll * sms) blocks = 8ll * sms;
+  const auto kernel = fmt == FG_E4M3 ? fg::moe_dispatch_kernel<0> : fg::moe_dispatch_kernel<1>;
+  return launch(kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, 1, p, chunks);
+}
+
+static fg_status combine_check(int T, int k, int M, int N) {
+  if (T < 0 || k < 0 || M < 0 || N < 0) return FG_ERR_INVALID_ARG;
+  if (N % 8 != 0) return FG_ERR_ALIGNMENT;
+  if (k > fg::kRowsMaxK) return FG_ERR_UNSUPPORTED;
+  return FG_OK;
+}
+
+fg_status fg_moe_combine(const void* C, const int* rows, const float* weights, void* out, int T, int k, int M, int N,
+                         void* stream) {
+  const fg_status bad = combine_check(T, k, M, N);
+  if (bad != FG_OK) return bad;
+  if (T == 0 || N == 0) return FG_OK;
+  if (!out || (k > 0 && (!rows || (M > 0 && !C)))) return FG_ERR_INVALID_ARG;
+  if (!aligned(C, 16) || !aligned(out, 16) || !aligned(rows, 4) || !aligned(weights, 4)) return FG_ERR_ALIGNMENT;
+  const int sms = sm_count();
+  if (sms <= 0) return FG_ERR_CUDA;
+  fg::CombineParams p;
+  p.C = static_cast<const __nv_bfloat16*>(C);
+  p.rows = rows;
+  p.weights = weights;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.T = T;
+  p.k = k;
+  p.N = N;
+  p.M = M;
+  const int chunks = static_cast<int>(cdiv(N, 256));
+  long long blocks = cdiv(static_cast<long long>(T) * chunks, 8);
+  if (blocks > 8ll * sms) blocks = 8ll * sms;
+  return launch(fg::moe_combine_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, 1, p, chunks);
+}
+
+fg_status fg_moe_combine_backward(const void* grad_out, const void* C, const int* rows, const float* weights,
+                                  void* grad_C, float* grad_weights, int T, int k, int M, int N, void* stream) {
+  const fg_status bad = combine_check(T, k, M, N);
+  if (bad != FG_OK) return bad;
+  if (T == 0 || k == 0) return FG_OK;
+  if (!rows || !weights || !grad_weights || (N > 0 && (!grad_out || (M > 0 && (!C || !grad_C)))))
+    return FG_ERR_INVALID_ARG;
+  if (!aligned(grad_out, 16) || !aligned(C, 16) || !aligned(grad_C, 16) || !aligned(rows, 4) || !aligned(weights, 4) ||
+      !aligned(grad_weights, 4))
+    return FG_ERR_ALIGNMENT;
+  const int sms = sm_count();
+  if (sms <= 0) return FG_ERR_CUDA;
+  fg::CombineGradParams p;
+  p.grad_out = static_cast<const __nv_bfloat16*>(grad_out);
+  p.C = static_cast<const __nv_bfloat16*>(C);
+  p.rows = rows;
+  p.weights = weights;
+  p.grad_C = static_cast<__nv_bfloat16*>(grad_C);
+  p.grad_weights = grad_weights;
+  p.T = T;
+  p.k = k;
+  p.N = N;
+  p.M = M;
+  const int blocks = T < 8 * sms ? T : 8 * sms;
+  return launch(fg::moe_combine_backward_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, 1, p);
+}
+
+fg_status fg_lora_add(const void* C, const void* x, const void* lora_a, const void* lora_b, const int* adapters,
+                      const float* scaling, void* out, int M, int N, int K, int R, int L, void* stream) {
+  if (M < 0 || N < 0 || K < 0 || R < 0 || L < 0) return FG_ERR_INVALID_ARG;
+  if (K % 16 != 0 || N % 8 != 0 || R % 8 != 0) return FG_ERR_ALIGNMENT;
+  if (R > fg::kLoraMaxRank) return FG_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return FG_OK;
+  if (!C || !out || !adapters) return FG_ERR_INVALID_ARG;
+  if (K == 0 || R == 0) L = 0;  // no adapter adds anything
+  if (L > 0 && (!x || !lora_a || !lora_b)) return FG_ERR_INVALID_ARG;
+  if (!aligned(C, 16) || !aligned(x, 16) || !aligned(lora_a, 16) || !aligned(lora_b, 16) || !aligned(out, 16) ||
+      !aligned(adapters, 4) || !aligned(scaling, 4))
+    return FG_ERR_ALIGNMENT;
+  fg::LoraParams p;
+  p.C = static_cast<const __nv_bfloat16*>(C);
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.a = static_cast<const __nv_bfloat16*>(lora_a);
+  p.b = static_cast<const __nv_bfloat16*>(lora_b);
+  p.adapters = adapters;
+  p.scaling = scaling;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.R = R;
+  p.L = L;
+  if (R <= 8) return lora_launch<1>(p, stream);
+  if (R <= 16) return lora_launch<2>(p, stream);
+  if (R <= 32) return lora_launch<4>(p, stream);
+  if (R <= 64) return lora_launch<8>(p, stream);
+  return lora_launch<16>(p, stream);
+}
+
+}  // extern "C"
