@@ -15,7 +15,7 @@ COMMON = [CSRC / "fp8_cast_kernels.cuh", CSRC / "sm100_ptx.cuh", ROOT / "include
 SOURCES = {
     CSRC / "fp8gemm_api.cu": COMMON + [CSRC / "fp8_gemm_kernels.cuh", CSRC / "fp8gemm_jit.h"],
     CSRC / "operators_api.cu": COMMON + [CSRC / "moe_route_kernels.cuh", CSRC / "moe_rows_kernels.cuh",
-                                         CSRC / "lora_kernels.cuh"],
+                                         CSRC / "lora_kernels.cuh", CSRC / "cluster_ptx.cuh"],
 }
 
 NVCC_FLAGS = [

@@ -11,7 +11,9 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cstdint>
+#include <cstring>
 
+#include "cluster_ptx.cuh"
 #include "sm100_ptx.cuh"
 
 namespace fg {
@@ -19,16 +21,15 @@ namespace fg {
 constexpr int kRouteThreads = 256;
 constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kRouteMaxK = 32;
+constexpr int kRouteMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <typename T>
-__device__ __forceinline__ float to_f32(T v);
-template <>
-__device__ __forceinline__ float to_f32<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <>
-__device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+__device__ __forceinline__ uint32_t bits_of(float v) { return __float_as_uint(v); }
+__device__ __forceinline__ uint32_t bits_of(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
+__device__ __forceinline__ uint32_t bits_of(__half v) { return __half_as_ushort(v); }
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 template <typename T>
 __device__ __forceinline__ T from_f32(float v);
 template <>
@@ -38,27 +39,68 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { retu
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-// Order-preserving key of a logit: larger logit, larger key; 0 for -inf and NaN (never chosen), and
-// -0 and +0 alike.
-__device__ __forceinline__ uint32_t logit_key(float v) {
-  if (!(v > -INFINITY)) return 0u;
-  const uint32_t u = __float_as_uint(v + 0.0f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float key_logit(uint32_t key) {
-  return __uint_as_float((key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key);
-}
+// Orders a row's choices: a larger key is an earlier choice.  The upper part is the logit's bits made
+// monotonic, the lower one counts columns down, so that equal logits come lowest expert first; 0 for
+// logits that are never chosen (-inf, NaN, no column).  16-bit logits share one 32-bit word with
+// their column, which one warp reduction orders; fp32 logits take 64 bits and two.
+template <typename T>
+struct RouteKey {
+  typedef uint32_t type;
+  static __device__ __forceinline__ type make(T v, float f, int col) {
+    uint32_t u = bits_of(v);
+    if (u == 0x8000u) u = 0;  // -0 and +0 are equal
+    u = (u & 0x8000u) ? (~u & 0xFFFFu) : (u | 0x8000u);
+    return f > -INFINITY ? (u << 16) | static_cast<uint32_t>(0xFFFF - col) : 0u;
+  }
+  static __device__ __forceinline__ int col(type k) { return 0xFFFF - static_cast<int>(k & 0xFFFFu); }
+  static __device__ __forceinline__ float logit(type k) {
+    const uint32_t u = k >> 16;
+    const unsigned short h = static_cast<unsigned short>((u & 0x8000u) ? (u & 0x7FFFu) : (~u & 0xFFFFu));
+    if constexpr (sizeof(T) == 2) {
+      T t;
+      memcpy(&t, &h, 2);
+      return to_f32(t);
+    }
+    return 0.0f;
+  }
+};
+template <>
+struct RouteKey<float> {
+  typedef unsigned long long type;
+  static __device__ __forceinline__ type make(float v, float, int col) {
+    const uint32_t u = __float_as_uint(v + 0.0f);  // -0 and +0 are equal
+    const uint32_t key = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    return v > -INFINITY ? (static_cast<type>(key) << 32) | static_cast<uint32_t>(0xFFFF - col) : 0ull;
+  }
+  static __device__ __forceinline__ int col(type k) { return 0xFFFF - static_cast<int>(k & 0xFFFFu); }
+  static __device__ __forceinline__ float logit(type k) {
+    const uint32_t u = static_cast<uint32_t>(k >> 32);
+    return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
+  }
+};
 
 // e^(x - high), high the row's largest logit.  The difference is formed first: with the type's lowest
-// value in every place of a row, a product with log2(e) before it would overflow.
-__device__ __forceinline__ float softmax_exp(float x, float high) { return exp2f((x - high) * kLog2e); }
+// value in every place of a row, a product with log2(e) before it would overflow.  ex2.approx is within
+// 2^-22 relative; results below 2^-126 become 0.
+__device__ __forceinline__ float softmax_exp(float x, float high) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((x - high) * kLog2e));
+  return y;
+}
 
 // Reductions over the LPR lanes that hold one row (LPR a power of two).
-template <int LPR>
-__device__ __forceinline__ float row_sum(float v) {
+template <int LPR, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N]) {
 #pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int o = LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+}
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x) {
+  float v[1] = {x};
+  row_sums<LPR>(v);
+  return v[0];
 }
 template <int LPR>
 __device__ __forceinline__ float row_max(float v) {
@@ -67,7 +109,7 @@ __device__ __forceinline__ float row_max(float v) {
   return v;
 }
 template <int LPR>
-__device__ __forceinline__ uint32_t row_max_u32(uint32_t v) {
+__device__ __forceinline__ uint32_t row_best(uint32_t v) {
   if constexpr (LPR == 32) {
     return __reduce_max_sync(0xffffffffu, v);
   } else {
@@ -77,13 +119,52 @@ __device__ __forceinline__ uint32_t row_max_u32(uint32_t v) {
   }
 }
 template <int LPR>
-__device__ __forceinline__ int row_min_s32(int v) {
+__device__ __forceinline__ unsigned long long row_best(unsigned long long v) {
   if constexpr (LPR == 32) {
-    return __reduce_min_sync(0xffffffffu, v);
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(v >> 32));
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
+    return (static_cast<unsigned long long>(hi) << 32) | lo;
   } else {
 #pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = LPR / 2; o > 0; o >>= 1) {
+      const unsigned long long w = __shfl_xor_sync(0xffffffffu, v, o);
+      if (w > v) v = w;
+    }
     return v;
+  }
+}
+
+// Batcher's odd-even merge sort of registers, largest first: sort_falling sorts v[LO .. LO + N), merge_falling merges
+// the sorted halves of its elements LO, LO + STEP, ...
+template <int A, int B, typename K, int M>
+__device__ __forceinline__ void order_falling(K (&v)[M]) {
+  const K a = v[A], b = v[B];
+  v[A] = a > b ? a : b;
+  v[B] = a > b ? b : a;
+}
+template <int LO, int END, int STEP, typename K, int M>
+__device__ __forceinline__ void order_pairs(K (&v)[M]) {
+  if constexpr (LO + STEP < END) {
+    order_falling<LO, LO + STEP>(v);
+    order_pairs<LO + 2 * STEP, END, STEP>(v);
+  }
+}
+template <int LO, int N, int STEP, typename K, int M>
+__device__ __forceinline__ void merge_falling(K (&v)[M]) {
+  if constexpr (2 * STEP < N) {
+    merge_falling<LO, N, 2 * STEP>(v);
+    merge_falling<LO + STEP, N, 2 * STEP>(v);
+    order_pairs<LO + STEP, LO + N, STEP>(v);
+  } else {
+    order_falling<LO, LO + STEP>(v);
+  }
+}
+template <int LO, int N, typename K, int M>
+__device__ __forceinline__ void sort_falling(K (&v)[M]) {
+  if constexpr (N > 1) {
+    sort_falling<LO, N / 2>(v);
+    sort_falling<LO + N / 2, N / 2>(v);
+    merge_falling<LO, N, 1>(v);
   }
 }
 
@@ -94,25 +175,24 @@ __device__ __forceinline__ int route_col(int i, int sub) {
   return (i / V * LPR + sub) * V + i % V;
 }
 
-// One row's values of this lane; columns at or past E read as -inf.  V > 1: E % V == 0 and the rows
-// 16-byte aligned (V * sizeof(T) == 16).
+// One row's values of this lane, as they are; columns at or past E read as -inf.  V > 1: E % V == 0
+// and the rows 16-byte aligned (V * sizeof(T) == 16).
 template <typename T, int LPR, int NPL, int V>
-__device__ __forceinline__ void load_logits(const T* row, int E, int sub, float (&x)[NPL]) {
+__device__ __forceinline__ void load_logits(const T* row, int E, int sub, T (&x)[NPL]) {
 #pragma unroll
   for (int i = 0; i < NPL; i += V) {
     const int c = route_col<LPR, V>(i, sub);
     if constexpr (V == 1) {
-      x[i] = c < E ? to_f32(row[c]) : -INFINITY;
+      x[i] = c < E ? row[c] : from_f32<T>(-INFINITY);
     } else {
+      uint4 raw;
       if (c < E) {
-        const uint4 raw = *reinterpret_cast<const uint4*>(row + c);
-        const T* t = reinterpret_cast<const T*>(&raw);
-#pragma unroll
-        for (int v = 0; v < V; ++v) x[i + v] = to_f32(t[v]);
+        raw = *reinterpret_cast<const uint4*>(row + c);
       } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) x[i + v] = -INFINITY;
+        const uint32_t none = sizeof(T) == 4 ? 0xFF800000u : bits_of(from_f32<T>(-INFINITY)) * 0x10001u;
+        raw = make_uint4(none, none, none, none);
       }
+      memcpy(&x[i], &raw, 16);
     }
   }
 }
@@ -130,16 +210,46 @@ struct RouteParams {
   int T, E, k, chunks, rows_per_chunk, renorm;
 };
 
+// What the sums over a sequence give.  Called by all threads of one CTA; thread e < E holds column e's
+// sum of p and count; rows: the routed tokens (same in every thread).
+__device__ __forceinline__ void route_finish(const RouteParams& p, int seq, float sum, int n, int rows, float* s_red,
+                                             int* s_total) {
+  const int e = threadIdx.x, warps = blockDim.x / 32;
+  const int here = __reduce_add_sync(0xffffffffu, e < p.E ? n : 0);
+  if (e == 0) *s_total = 0;
+  __syncthreads();
+  if ((e & 31) == 0 && here) atomicAdd(s_total, here);
+  __syncthreads();
+  const float total = static_cast<float>(max(*s_total, 1)) * static_cast<float>(max(rows, 1));
+  const float slope = static_cast<float>(p.E) * static_cast<float>(n) / total;
+  if (e < p.E) {
+    p.counts[static_cast<size_t>(seq) * p.E + e] = n;
+    p.slope[static_cast<size_t>(seq) * p.E + e] = slope;
+  }
+  float v = row_sum<32>(e < p.E ? slope * sum : 0.0f);
+  if ((e & 31) == 0) s_red[e >> 5] = v;
+  __syncthreads();
+  if (e < 32) {
+    v = row_sum<32>(e < warps ? s_red[e] : 0.0f);
+    if (e == 0) p.loss[seq] = v;
+  }
+}
+
 // Forward, one CTA per (chunk of rows, sequence).  LPR lanes hold a row, NPL values each, so a warp
-// works on 32 / LPR rows at once.
-template <typename T, int LPR, int NPL, int V>
+// works on 32 / LPR rows at once; the next rows are loaded while the present ones are worked on.  Bound
+// by instructions, about 300 per row of 256: each lane sorts its keys once (a network in registers), then every choice is one
+// reduction over the heads of the lanes' lists and a shift in the winner's.
+// CLUSTER: the sequence's CTAs are one cluster, whose first CTA sums the others' parts over distributed
+// shared memory and finishes; otherwise the parts go to memory for moe_route_finish_kernel.
+template <typename T, int LPR, int NPL, int V, bool CLUSTER>
 __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteParams p) {
+  typedef RouteKey<T> Key;
+  typedef typename Key::type K;
   constexpr int RPW = 32 / LPR;
   constexpr int EP = LPR * NPL;
   __shared__ int s_cnt[EP + 1];
   __shared__ float s_sum[kRouteWarps][EP];
-  __shared__ float s_w[kRouteWarps][RPW][kRouteMaxK];
-  __shared__ int s_id[kRouteWarps][RPW][kRouteMaxK];
+  __shared__ K s_key[kRouteWarps][RPW][kRouteMaxK];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane % LPR, rw = lane / LPR;
   const int seq = blockIdx.y, chunk = blockIdx.x;
@@ -153,64 +263,67 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
   for (int i = 0; i < NPL; ++i) acc[i] = 0.0f;
   const int first = chunk * p.rows_per_chunk;
   const int last = min(p.T, first + p.rows_per_chunk);
-  for (int r0 = first + warp * RPW; r0 < last; r0 += kRouteWarps * RPW) {
+  const size_t base = static_cast<size_t>(seq) * p.T;
+  const T* logits = static_cast<const T*>(p.logits);
+  T next[NPL];
+  bool next_live = false;
+  auto fetch = [&](int r0) {  // rows behind the last one repeat it and are dropped later
+    const int r = min(r0 + rw, last - 1);
+    next_live = !p.mask || p.mask[base + r];
+    load_logits<T, LPR, NPL, V>(logits + (base + r) * p.E, p.E, sub, next);
+  };
+  int r0 = first + warp * RPW;
+  if (r0 < last) fetch(r0);
+  for (; r0 < last; r0 += kRouteWarps * RPW) {
     const int r = r0 + rw;
-    const size_t row = static_cast<size_t>(seq) * p.T + min(r, last - 1);
-    const bool live = r < last && (!p.mask || p.mask[row]);
+    const size_t row = base + r;
+    const bool live = r < last && next_live;
     float x[NPL];
-    uint32_t key[NPL];
-    load_logits<T, LPR, NPL, V>(static_cast<const T*>(p.logits) + row * p.E, p.E, sub, x);
-    uint32_t best = 0;
+    K key[NPL];
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      key[i] = live ? logit_key(x[i]) : 0u;
-      best = max(best, key[i]);
+      x[i] = to_f32(next[i]);
+      key[i] = live ? Key::make(next[i], x[i], route_col<LPR, V>(i, sub)) : K(0);
     }
-    best = row_max_u32<LPR>(best);
+    if (r0 + kRouteWarps * RPW < last) fetch(r0 + kRouteWarps * RPW);
+    sort_falling<0, NPL>(key);
+    K best = row_best<LPR>(key[0]);
     const bool routed = best != 0;
-    const float high = routed ? key_logit(best) : 0.0f;
+    const float high = routed ? Key::logit(best) : 0.0f;
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
       x[i] = softmax_exp(x[i], high);
       sum += x[i];
     }
-    sum = row_sum<LPR>(sum);
-    const float inv = 1.0f / sum;
-    if (routed) {
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) acc[i] += x[i] * inv;
-    }
-    // the k largest keys, one at a time; among equal keys the lowest column
-    float top = 0.0f;
     for (int j = 0; j < p.k; ++j) {
-      int col = 0x7fffffff;
+      if (sub == j % LPR) s_key[warp][rw][j] = best;
+      if (key[0] == best) {
 #pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if (key[i] == best) col = min(col, route_col<LPR, V>(i, sub));
-      col = row_min_s32<LPR>(col);
-      const float w = best ? softmax_exp(key_logit(best), high) : 0.0f;
-      top += w;
-      if (sub == j % LPR) {
-        s_id[warp][rw][j] = best ? col : -1;
-        s_w[warp][rw][j] = w;
+        for (int i = 0; i + 1 < NPL; ++i) key[i] = key[i + 1];
+        key[NPL - 1] = 0;
       }
-      uint32_t next = 0;
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        if (key[i] == best && route_col<LPR, V>(i, sub) == col) key[i] = 0;
-        next = max(next, key[i]);
-      }
-      best = row_max_u32<LPR>(next);
+      if (j + 1 < p.k) best = row_best<LPR>(key[0]);
     }
     __syncwarp();
+    float sums[2] = {sum, 0.0f};  // over all columns; over the choices
+    for (int j = sub; j < p.k; j += LPR) {
+      const K c = s_key[warp][rw][j];
+      if (c) sums[1] += softmax_exp(Key::logit(c), high);
+    }
+    row_sums<LPR>(sums);
+    const float inv = 1.0f / sums[0];
+    if (routed) {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) acc[i] = fmaf(x[i], inv, acc[i]);
+    }
     if (r < last) {
-      const float scale = routed ? 1.0f / (p.renorm ? top : sum) : 0.0f;
+      const float scale = p.renorm ? 1.0f / sums[1] : inv;
       for (int j = sub; j < p.k; j += LPR) {
-        const int id = s_id[warp][rw][j];
-        p.ids[row * p.k + j] = id;
-        p.weights[row * p.k + j] = id >= 0 ? s_w[warp][rw][j] * scale : 0.0f;
-        if (id >= 0) atomicAdd(&s_cnt[id], 1);
+        const K c = s_key[warp][rw][j];
+        p.ids[row * p.k + j] = c ? Key::col(c) : -1;
+        p.weights[row * p.k + j] = c ? softmax_exp(Key::logit(c), high) * scale : 0.0f;
+        if (c) atomicAdd(&s_cnt[Key::col(c)], 1);
       }
       if (sub == 0 && routed) atomicAdd(&s_cnt[EP], 1);
     }
@@ -229,47 +342,77 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < kRouteWarps; ++w) v += s_sum[w][e];
-    p.part_p[slot * p.E + e] = v;
-    p.part_n[slot * (p.E + 1) + e] = s_cnt[e];
+    if constexpr (CLUSTER) {
+      s_sum[0][e] = v;
+    } else {
+      p.part_p[slot * p.E + e] = v;
+      p.part_n[slot * (p.E + 1) + e] = s_cnt[e];
+    }
   }
-  if (threadIdx.x == 0) p.part_n[slot * (p.E + 1) + p.E] = s_cnt[EP];
+  if constexpr (CLUSTER) {
+    __shared__ float s_red[kRouteWarps];
+    __shared__ int s_total;
+    cluster_sync_all();
+    if (chunk == 0) {
+      static_assert(EP <= kRouteThreads, "one column per thread");
+      float v = 0.0f;
+      int n = 0, rows = 0;
+      const int e = threadIdx.x;
+      const uint32_t sum_at = smem_addr(&s_sum[0][min(e, EP - 1)]), n_at = smem_addr(&s_cnt[min(e, EP - 1)]),
+                     rows_at = smem_addr(&s_cnt[EP]);
+      for (int c = 0; c < p.chunks; ++c) {
+        v += ld_dsmem_f32(mapa_shared(sum_at, c));
+        n += __float_as_int(ld_dsmem_f32(mapa_shared(n_at, c)));
+        rows += __float_as_int(ld_dsmem_f32(mapa_shared(rows_at, c)));
+      }
+      cluster_sync_all();  // the parts have been read
+      route_finish(p, seq, v, n, rows, s_red, &s_total);
+    } else {
+      cluster_sync_all();  // no CTA leaves before its part has been read
+    }
+  } else {
+    if (threadIdx.x == 0) p.part_n[slot * (p.E + 1) + p.E] = s_cnt[EP];
+  }
 }
 
-// Sums of the chunks of one sequence (in chunk order), then its counts, slopes and loss.
+// Sums of the chunks of one sequence in a fixed order, then its counts, slopes and loss.  1024 threads:
+// as many parts of the chunks as columns leave room for, summed side by side.
 __global__ void __launch_bounds__(1024) moe_route_finish_kernel(const RouteParams p) {
+  __shared__ float s_part[1024];
+  __shared__ int s_cnt[1024];
   __shared__ float s_red[32];
-  __shared__ int s_n[2];
+  __shared__ int s_total, s_rows;
   const int seq = blockIdx.x;
-  if (threadIdx.x < 2) s_n[threadIdx.x] = 0;
+  if (threadIdx.x == 0) s_rows = 0;
   __syncthreads();
   pdl_wait_prior_grid();
   pdl_launch_dependents();
   const size_t slot = static_cast<size_t>(seq) * p.chunks;
-  const int e = threadIdx.x;
+  const int cols = (p.E + 31) / 32 * 32, parts = 1024 / cols;
+  const int e = threadIdx.x % cols, part = threadIdx.x / cols;
   float sum = 0.0f;
   int n = 0;
-  if (e < p.E) {
-    for (int c = 0; c < p.chunks; ++c) {
+  if (e < p.E && part < parts) {
+#pragma unroll 8
+    for (int c = part; c < p.chunks; c += parts) {
       sum += p.part_p[(slot + c) * p.E + e];
       n += p.part_n[(slot + c) * (p.E + 1) + e];
     }
-    p.counts[static_cast<size_t>(seq) * p.E + e] = n;
-    if (n) atomicAdd(&s_n[0], n);
   }
+  s_part[threadIdx.x] = sum;
+  s_cnt[threadIdx.x] = n;
   int rows = 0;
-  for (int c = e; c < p.chunks; c += blockDim.x) rows += p.part_n[(slot + c) * (p.E + 1) + p.E];
-  if (rows) atomicAdd(&s_n[1], rows);
+  for (int c = threadIdx.x; c < p.chunks; c += 1024) rows += p.part_n[(slot + c) * (p.E + 1) + p.E];
+  if (rows) atomicAdd(&s_rows, rows);
   __syncthreads();
-  const float total = static_cast<float>(max(s_n[0], 1)) * static_cast<float>(max(s_n[1], 1));
-  const float slope = static_cast<float>(p.E) * static_cast<float>(n) / total;
-  if (e < p.E) p.slope[static_cast<size_t>(seq) * p.E + e] = slope;
-  float v = row_sum<32>(e < p.E ? slope * sum : 0.0f);
-  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    v = row_sum<32>(threadIdx.x < blockDim.x / 32 ? s_red[threadIdx.x] : 0.0f);
-    if (threadIdx.x == 0) p.loss[seq] = v;
+  if (part == 0) {
+    for (int q = 1; q < parts; ++q) {
+      sum += s_part[q * cols + e];
+      n += s_cnt[q * cols + e];
+    }
   }
+  // columns past E (and threads of other parts) hold nothing
+  route_finish(p, seq, sum, threadIdx.x < p.E ? n : 0, s_rows, s_red, &s_total);
 }
 
 struct RouteGradParams {
@@ -282,14 +425,16 @@ struct RouteGradParams {
   int T, E, k, rows_per_chunk, renorm;
 };
 
-// Backward.  With h_e = grad_loss * slope_e (+ grad_weights_j at the chosen columns when the weights
-// are not renormalised):  d l = p (h - sum p h).  Renormalised weights are the softmax w over the
-// chosen logits: d l_j += w_j (g_j - sum w g) there.  Rows without a choice get zeros.
+// Backward.  With u_e = e^(l_e - max), h_e = grad_loss * slope_e and g_j the gradient of weight j:
+//   not renormalised:  d l_e = p_e (h_e - (sum u h + sum_j u_j g_j) / sum u)   (+ p_j g_j at the choices)
+//   renormalised:      d l_e = p_e (h_e - sum u h / sum u)  (+ w_j (g_j - sum_j w g) at the choices),
+// w the softmax over the chosen logits.  All four sums are reduced together.  Rows without a choice get
+// zeros.  What the choices add goes through a row of shared memory, which is zero between rows.
 template <typename T, int LPR, int NPL, int V>
 __global__ void __launch_bounds__(kRouteThreads) moe_route_backward_kernel(const RouteGradParams p) {
   constexpr int RPW = 32 / LPR;
   constexpr int EP = LPR * NPL;
-  __shared__ float s_add[kRouteWarps][RPW][EP];  // what the chosen columns add; zero between rows
+  __shared__ __align__(16) float s_add[kRouteWarps][RPW][EP];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane % LPR, rw = lane / LPR;
   const int seq = blockIdx.y;
@@ -298,91 +443,118 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_backward_kernel(const
   pdl_wait_prior_grid();
   pdl_launch_dependents();
   float* add = s_add[warp][rw];
-  float h0[NPL];
+  float h[NPL];
   const float g = p.grad_loss ? p.grad_loss[seq] : 0.0f;
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
     const int c = route_col<LPR, V>(i, sub);
-    h0[i] = p.grad_loss && c < p.E ? g * p.slope[static_cast<size_t>(seq) * p.E + c] : 0.0f;
+    h[i] = p.grad_loss && c < p.E ? g * p.slope[static_cast<size_t>(seq) * p.E + c] : 0.0f;
   }
   const int first = blockIdx.x * p.rows_per_chunk;
   const int last = min(p.T, first + p.rows_per_chunk);
-  for (int r0 = first + warp * RPW; r0 < last; r0 += kRouteWarps * RPW) {
+  const size_t base = static_cast<size_t>(seq) * p.T;
+  const T* all = static_cast<const T*>(p.logits);
+  T next[NPL];
+  int next_id = -1;
+  float next_g = 0.0f;
+  auto choice = [&](size_t row, int j, int& id, float& gw) {
+    id = p.ids[row * p.k + j];
+    if (id < 0 || id >= p.E) id = -1;
+    gw = p.grad_weights && id >= 0 ? p.grad_weights[row * p.k + j] : 0.0f;
+  };
+  auto fetch = [&](int r0) {
+    const size_t row = base + min(r0 + rw, last - 1);
+    load_logits<T, LPR, NPL, V>(all + row * p.E, p.E, sub, next);
+    next_id = -1;
+    if (sub < p.k) choice(row, sub, next_id, next_g);
+  };
+  int r0 = first + warp * RPW;
+  if (r0 < last) fetch(r0);
+  for (; r0 < last; r0 += kRouteWarps * RPW) {
     const int r = r0 + rw;
-    const size_t row = static_cast<size_t>(seq) * p.T + min(r, last - 1);
-    const T* logits = static_cast<const T*>(p.logits) + row * p.E;
-    const int* ids = p.ids + row * p.k;
+    const size_t row = base + min(r, last - 1);
+    const T* logits = all + row * p.E;
     float x[NPL];
-    load_logits<T, LPR, NPL, V>(logits, p.E, sub, x);
-    bool any = false;
-    for (int j = sub; j < p.k; j += LPR) any |= ids[j] >= 0 && ids[j] < p.E;
-    const bool routed = row_max<LPR>(any ? 1.0f : 0.0f) > 0.0f;
     float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) m = fmaxf(m, x[i]);
+    for (int i = 0; i < NPL; ++i) {
+      x[i] = to_f32(next[i]);
+      m = fmaxf(m, x[i]);
+    }
+    const int id = next_id;
+    const float gw = next_g;
+    if (r0 + kRouteWarps * RPW < last) fetch(r0 + kRouteWarps * RPW);
     const float high = row_max<LPR>(m);
-    float sum = 0.0f;
+    // sums of u, of u h, of u over the choices, of u g over the choices
+    float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
       x[i] = softmax_exp(x[i], high);
-      sum += x[i];
+      sums[0] += x[i];
+      sums[1] = fmaf(x[i], h[i], sums[1]);
     }
-    const float inv = 1.0f / row_sum<LPR>(sum);
-    if (p.grad_weights) {
-      const float* gw = p.grad_weights + row * p.k;
-      float top = 0.0f, dot = 0.0f;
-      if (p.renorm) {
-        for (int j = sub; j < p.k; j += LPR) {
-          const int id = ids[j];
-          if (id < 0 || id >= p.E) continue;
-          const float w = softmax_exp(to_f32(logits[id]), high);
-          top += w;
-          dot += w * gw[j];
-        }
-        top = 1.0f / row_sum<LPR>(top);
-        dot = row_sum<LPR>(dot) * top;
-      }
-      for (int j = sub; j < p.k; j += LPR) {
-        const int id = ids[j];
-        if (id < 0 || id >= p.E) continue;
-        atomicAdd(&add[id], p.renorm ? softmax_exp(to_f32(logits[id]), high) * top * (gw[j] - dot) : gw[j]);
-      }
-      __syncwarp();
+    bool any = id >= 0;
+    const float u = id >= 0 ? softmax_exp(to_f32(logits[id]), high) : 0.0f;
+    sums[2] = u;
+    sums[3] = u * gw;
+    for (int j = sub + LPR; j < p.k; j += LPR) {
+      int id2;
+      float gw2;
+      choice(row, j, id2, gw2);
+      if (id2 < 0) continue;
+      any = true;
+      const float u2 = softmax_exp(to_f32(logits[id2]), high);
+      sums[2] += u2;
+      sums[3] = fmaf(u2, gw2, sums[3]);
     }
-    float dot = 0.0f;
-    float a[NPL];
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      a[i] = add[route_col<LPR, V>(i, sub)];
-      x[i] *= inv;
-      dot += x[i] * (p.renorm ? h0[i] : h0[i] + a[i]);
-    }
-    dot = row_sum<LPR>(dot);
-    __syncwarp();
-    if (p.grad_weights) {
-      for (int j = sub; j < p.k; j += LPR) {
-        const int id = ids[j];
-        if (id >= 0 && id < p.E) add[id] = 0.0f;
+    const uint32_t votes = __ballot_sync(0xffffffffu, any);
+    const bool routed = (votes >> (rw * LPR)) & (LPR == 32 ? 0xffffffffu : (1u << (LPR & 31)) - 1);
+    row_sums<LPR>(sums);
+    const float inv = 1.0f / sums[0];
+    const float top = p.renorm ? 1.0f / sums[2] : inv;
+    const float mean = p.renorm ? sums[3] * top : 0.0f;
+    const float dot = (p.renorm ? sums[1] : sums[1] + sums[3]) * inv;
+    if (p.grad_weights) {  // shared atomics: a choice may stand twice
+      if (id >= 0) atomicAdd(&add[id], u * top * (gw - mean));
+      for (int j = sub + LPR; j < p.k; j += LPR) {
+        int id2;
+        float gw2;
+        choice(row, j, id2, gw2);
+        if (id2 >= 0) atomicAdd(&add[id2], softmax_exp(to_f32(logits[id2]), high) * top * (gw2 - mean));
       }
       __syncwarp();
     }
-    if (r >= last) continue;
     T* out = static_cast<T*>(p.grad_logits) + row * p.E;
 #pragma unroll
     for (int i = 0; i < NPL; i += V) {
       const int c = route_col<LPR, V>(i, sub);
-      if (c >= p.E) continue;
       alignas(16) T t[V];
+      float a[V];
+      if constexpr (V % 4 == 0) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float d = p.renorm ? x[i + v] * (h0[i + v] - dot) + a[i + v]
-                                 : x[i + v] * (h0[i + v] + a[i + v] - dot);
-        t[v] = from_f32<T>(routed ? d : 0.0f);
+        for (int v = 0; v < V; v += 4) *reinterpret_cast<float4*>(a + v) = *reinterpret_cast<const float4*>(add + c + v);
+      } else {
+        a[0] = add[c];
       }
-      if constexpr (V == 1)
-        out[c] = t[0];
-      else
-        *reinterpret_cast<uint4*>(out + c) = *reinterpret_cast<const uint4*>(t);
+#pragma unroll
+      for (int v = 0; v < V; ++v) t[v] = from_f32<T>(routed ? fmaf(x[i + v] * inv, h[i + v] - dot, a[v]) : 0.0f);
+      if (c < p.E && r < last) {
+        if constexpr (V == 1)
+          out[c] = t[0];
+        else
+          *reinterpret_cast<uint4*>(out + c) = *reinterpret_cast<const uint4*>(t);
+      }
+    }
+    if (p.grad_weights) {
+      __syncwarp();
+      if (id >= 0) add[id] = 0.0f;
+      for (int j = sub + LPR; j < p.k; j += LPR) {
+        int id2;
+        float gw2;
+        choice(row, j, id2, gw2);
+        if (id2 >= 0) add[id2] = 0.0f;
+      }
+      __syncwarp();
     }
   }
 }

@@ -19,6 +19,8 @@ constexpr int kMaxDevices = 64;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
+
 int sm_count() {
   static std::atomic<int> cached[kMaxDevices];
   int dev = -1;
@@ -80,26 +82,42 @@ bool allow_smem(size_t bytes) {
   return true;
 }
 
-long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
-
 // ------------------------------------------------------------------------------------ the router
 size_t value_bytes(int dtype) { return dtype == FG_F32 ? 4 : 2; }
 bool valid_dtype(int dtype) { return dtype == FG_F32 || dtype == FG_BF16 || dtype == FG_F16; }
 
-// Rows of a sequence per CTA: few enough that the SMs hold about four CTAs each, a multiple of the
-// rows that the warps of a CTA take at once (at most 32).
-int route_rows_per_chunk(int S, int T, int sms) {
-  long long rows = cdiv(static_cast<long long>(S) * T, 4ll * sms);
-  rows = cdiv(rows, 32) * 32;
-  return static_cast<int>(rows < T ? rows : T);
+// Lanes that hold a row of E columns, and the rows that a CTA's warps take at once.
+int route_step(int E) { return fg::kRouteWarps * (E <= 64 ? 4 : E <= 128 ? 2 : 1); }
+
+// How a sequence of T rows is split over CTAs.  Up to four rows a warp of eight CTAs: one cluster per
+// sequence, which also finishes (one launch).  Otherwise chunks such that every SM gets about four
+// CTAs, and a second kernel finishes.
+struct RouteSplit {
+  int rows, chunks;  // rows per CTA, CTAs per sequence
+  bool cluster;
+};
+RouteSplit route_split(int S, int T, int E, int sms) {
+  RouteSplit r;
+  const int step = route_step(E);
+  r.cluster = E <= fg::kRouteThreads && T <= 4 * fg::kRouteMaxCluster * step;
+  const long long share = r.cluster ? cdiv(T, fg::kRouteMaxCluster) : cdiv(static_cast<long long>(S) * T, 4ll * sms);
+  const long long rows = cdiv(share, step) * step;
+  r.rows = static_cast<int>(rows < T ? rows : T);
+  r.chunks = static_cast<int>(cdiv(T, r.rows));
+  return r;
 }
 
 template <typename T, int LPR, int NPL, int V>
-fg_status route_launch(const fg::RouteParams& p, int S, void* stream) {
-  return launch(fg::moe_route_kernel<T, LPR, NPL, V>, dim3(p.chunks, S), fg::kRouteThreads, 0, stream, 1, p);
+fg_status route_launch(const fg::RouteParams& p, int S, bool cluster, void* stream) {
+  if constexpr (LPR * NPL <= fg::kRouteThreads) {
+    if (cluster)
+      return launch(fg::moe_route_kernel<T, LPR, NPL, V, true>, dim3(p.chunks, S), fg::kRouteThreads, 0, stream,
+                    p.chunks, p);
+  }
+  return launch(fg::moe_route_kernel<T, LPR, NPL, V, false>, dim3(p.chunks, S), fg::kRouteThreads, 0, stream, 1, p);
 }
 template <typename T, int LPR, int NPL, int V>
-fg_status route_launch(const fg::RouteGradParams& p, int S, void* stream) {
+fg_status route_launch(const fg::RouteGradParams& p, int S, bool, void* stream) {
   return launch(fg::moe_route_backward_kernel<T, LPR, NPL, V>, dim3(static_cast<unsigned>(cdiv(p.T, p.rows_per_chunk)), S),
                 fg::kRouteThreads, 0, stream, 1, p);
 }
@@ -107,30 +125,30 @@ fg_status route_launch(const fg::RouteGradParams& p, int S, void* stream) {
 // The instance that holds E columns: few lanes a row for few experts, 16-byte loads where each row
 // starts on a 16-byte boundary.
 template <typename T, typename P>
-fg_status route_pick(const P& p, int S, bool wide, void* stream) {
+fg_status route_pick(const P& p, int S, bool cluster, bool wide, void* stream) {
   constexpr int V = 16 / static_cast<int>(sizeof(T));
   const int E = p.E;
   if (wide) {
-    if (E <= 64) return route_launch<T, 8, 8, V>(p, S, stream);
-    if (E <= 128) return route_launch<T, 16, 8, V>(p, S, stream);
-    if (E <= 256) return route_launch<T, 32, 8, V>(p, S, stream);
-    if (E <= 512) return route_launch<T, 32, 16, V>(p, S, stream);
-    return route_launch<T, 32, 32, V>(p, S, stream);
+    if (E <= 64) return route_launch<T, 8, 8, V>(p, S, cluster, stream);
+    if (E <= 128) return route_launch<T, 16, 8, V>(p, S, cluster, stream);
+    if (E <= 256) return route_launch<T, 32, 8, V>(p, S, cluster, stream);
+    if (E <= 512) return route_launch<T, 32, 16, V>(p, S, cluster, stream);
+    return route_launch<T, 32, 32, V>(p, S, cluster, stream);
   }
-  if (E <= 8) return route_launch<T, 8, 1, 1>(p, S, stream);
-  if (E <= 32) return route_launch<T, 8, 4, 1>(p, S, stream);
-  if (E <= 64) return route_launch<T, 8, 8, 1>(p, S, stream);
-  if (E <= 128) return route_launch<T, 16, 8, 1>(p, S, stream);
-  if (E <= 256) return route_launch<T, 32, 8, 1>(p, S, stream);
-  if (E <= 512) return route_launch<T, 32, 16, 1>(p, S, stream);
-  return route_launch<T, 32, 32, 1>(p, S, stream);
+  if (E <= 8) return route_launch<T, 8, 1, 1>(p, S, cluster, stream);
+  if (E <= 32) return route_launch<T, 8, 4, 1>(p, S, cluster, stream);
+  if (E <= 64) return route_launch<T, 8, 8, 1>(p, S, cluster, stream);
+  if (E <= 128) return route_launch<T, 16, 8, 1>(p, S, cluster, stream);
+  if (E <= 256) return route_launch<T, 32, 8, 1>(p, S, cluster, stream);
+  if (E <= 512) return route_launch<T, 32, 16, 1>(p, S, cluster, stream);
+  return route_launch<T, 32, 32, 1>(p, S, cluster, stream);
 }
 
 template <typename P>
-fg_status route_dispatch(const P& p, int S, int dtype, bool wide, void* stream) {
-  if (dtype == FG_F32) return route_pick<float>(p, S, wide, stream);
-  if (dtype == FG_BF16) return route_pick<__nv_bfloat16>(p, S, wide, stream);
-  return route_pick<__half>(p, S, wide, stream);
+fg_status route_dispatch(const P& p, int S, int dtype, bool cluster, bool wide, void* stream) {
+  if (dtype == FG_F32) return route_pick<float>(p, S, cluster, wide, stream);
+  if (dtype == FG_BF16) return route_pick<__nv_bfloat16>(p, S, cluster, wide, stream);
+  return route_pick<__half>(p, S, cluster, wide, stream);
 }
 
 fg_status route_check(int dtype, int S, int T, int E, int k) {
@@ -139,17 +157,10 @@ fg_status route_check(int dtype, int S, int T, int E, int k) {
   return FG_OK;
 }
 
-struct RouteScratch {
-  int chunks, rows;
-  size_t p_bytes, bytes;
-};
-RouteScratch route_scratch(int S, int T, int E, int sms) {
-  RouteScratch r;
-  r.rows = T > 0 ? route_rows_per_chunk(S, T, sms) : 1;
-  r.chunks = static_cast<int>(cdiv(T, r.rows));
-  r.p_bytes = static_cast<size_t>(S) * r.chunks * E * 4;
-  r.bytes = r.p_bytes + static_cast<size_t>(S) * r.chunks * (E + 1) * 4;
-  return r;
+size_t route_part_bytes(int S, int E, const RouteSplit& r) { return static_cast<size_t>(S) * r.chunks * E * 4; }
+size_t route_scratch_bytes(int S, int E, const RouteSplit& r) {
+  if (r.cluster) return 0;
+  return route_part_bytes(S, E, r) + static_cast<size_t>(S) * r.chunks * (E + 1) * 4;
 }
 
 // ------------------------------------------------------------------------------------ row layouts
@@ -199,7 +210,7 @@ extern "C" {
 size_t fg_moe_route_scratch_bytes(int S, int T, int E) {
   if (S <= 0 || T <= 0 || E <= 0) return 0;
   const int sms = sm_count();
-  return sms > 0 ? route_scratch(S, T, E, sms).bytes : 0;
+  return sms > 0 ? route_scratch_bytes(S, E, route_split(S, T, E, sms)) : 0;
 }
 
 fg_status fg_moe_route(const void* logits, int dtype, const unsigned char* mask, int* ids, float* weights, int* counts,
@@ -208,15 +219,14 @@ fg_status fg_moe_route(const void* logits, int dtype, const unsigned char* mask,
   const fg_status bad = route_check(dtype, S, T, E, k);
   if (bad != FG_OK) return bad;
   if (S == 0) return FG_OK;
-  if (!counts || !loss || !slope || (T > 0 && (!logits || !ids || !weights || !scratch))) return FG_ERR_INVALID_ARG;
+  if (!counts || !loss || !slope || (T > 0 && (!logits || !ids || !weights))) return FG_ERR_INVALID_ARG;
   if (!aligned(logits, value_bytes(dtype)) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(counts, 4) ||
       !aligned(loss, 4) || !aligned(slope, 4) || !aligned(scratch, 4))
     return FG_ERR_ALIGNMENT;
   const int sms = sm_count();
   if (sms <= 0) return FG_ERR_CUDA;
-  const RouteScratch r = route_scratch(S, T, E, sms);
-  if (T > 0 && scratch_bytes < r.bytes) return FG_ERR_INVALID_ARG;
   fg::RouteParams p;
+  std::memset(&p, 0, sizeof(p));
   p.logits = logits;
   p.mask = mask;
   p.ids = ids;
@@ -224,21 +234,23 @@ fg_status fg_moe_route(const void* logits, int dtype, const unsigned char* mask,
   p.counts = counts;
   p.loss = loss;
   p.slope = slope;
-  p.part_p = static_cast<float*>(scratch);
-  p.part_n = reinterpret_cast<int*>(static_cast<char*>(scratch) + r.p_bytes);
   p.T = T;
   p.E = E;
   p.k = k;
-  p.chunks = r.chunks;
-  p.rows_per_chunk = r.rows;
   p.renorm = renormalize ? 1 : 0;
   if (T > 0) {
-    const size_t size = value_bytes(dtype);
-    const bool wide = aligned(logits, 16) && static_cast<size_t>(E) * size % 16 == 0;
-    const fg_status s = route_dispatch(p, S, dtype, wide, stream);
-    if (s != FG_OK) return s;
+    const RouteSplit r = route_split(S, T, E, sms);
+    const size_t need = route_scratch_bytes(S, E, r);
+    if (need > 0 && (!scratch || scratch_bytes < need)) return FG_ERR_INVALID_ARG;
+    p.part_p = static_cast<float*>(scratch);
+    p.part_n = need > 0 ? reinterpret_cast<int*>(static_cast<char*>(scratch) + route_part_bytes(S, E, r)) : nullptr;
+    p.chunks = r.chunks;
+    p.rows_per_chunk = r.rows;
+    const bool wide = aligned(logits, 16) && static_cast<size_t>(E) * value_bytes(dtype) % 16 == 0;
+    const fg_status s = route_dispatch(p, S, dtype, r.cluster, wide, stream);
+    if (s != FG_OK || r.cluster) return s;
   }
-  return launch(fg::moe_route_finish_kernel, dim3(S), static_cast<int>(cdiv(E, 32) * 32), 0, stream, 1, p);
+  return launch(fg::moe_route_finish_kernel, dim3(S), 1024, 0, stream, 1, p);
 }
 
 fg_status fg_moe_route_backward(const void* logits, int dtype, const int* ids, const float* slope,
@@ -264,10 +276,11 @@ fg_status fg_moe_route_backward(const void* logits, int dtype, const int* ids, c
   p.T = T;
   p.E = E;
   p.k = k;
-  p.rows_per_chunk = route_rows_per_chunk(S, T, sms);
+  const int step = route_step(E);
+  p.rows_per_chunk = static_cast<int>(cdiv(cdiv(static_cast<long long>(S) * T, 4ll * sms), step) * step);
   p.renorm = renormalize ? 1 : 0;
   const bool wide = aligned(logits, 16) && aligned(grad_logits, 16) && static_cast<size_t>(E) * size % 16 == 0;
-  return route_dispatch(p, S, dtype, wide, stream);
+  return route_dispatch(p, S, dtype, false, wide, stream);
 }
 
 long long fg_moe_layout_rows(long long pairs, int E) {

@@ -15,23 +15,32 @@ See include/fp8gemm.h for the definitions.
 """
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
-from . import FORMATS, _bf16, _cdiv, _check, _f32, _i32, _lib, _same_device, _stream, sfa_ld
+from . import FORMATS, _bf16, _cdiv, _check, _f32, _i32, _lib, _stream
 
 MAX_EXPERTS = 1024
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """Launch on `stream` (default: the current stream of `device`), with that stream current, so
-    that what is allocated meanwhile is not handed to other work of another stream too early."""
-    handle = _stream(stream, device)  # checks that the stream is the device's
-    with torch.cuda.device(device), (torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()):
-        yield handle
+# Calls of a decode step are as long as their host side, so each entry point goes straight to the C
+# ABI when it runs on the current device and stream, and otherwise once more with those made current.
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the handle without a Stream object
+
+
+def _elsewhere(device, stream) -> bool:
+    return stream is not None or device.index != torch.cuda.current_device()
+
+
+def _there(device, stream, call, *args, **kwargs):
+    """`call` with `device` and `stream` (None: the device's current one) current, so that what it
+    allocates is not handed to another stream's work too early."""
+    _stream(stream, device)  # checks that the stream is the device's
+    with torch.cuda.device(device):
+        if stream is None:
+            return call(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return call(*args, **kwargs)
 
 
 def _ptr(t):
@@ -51,9 +60,23 @@ def _logits(t: torch.Tensor):
 
 
 def _shaped(t: torch.Tensor, shape, what: str):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
+
+
+def _same_device_as(first, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != first.get_device():
+            raise ValueError(f"{name} is on {t.device}, the first operand on {first.device}")
+
+
+def _scratch(size, device):
+    """(tensor or None, its address): scratch of a call, kept by the caller until it has launched."""
+    if size == 0:
+        return None, None
+    t = torch.empty(size, dtype=torch.uint8, device=device)
+    return t, t.data_ptr()
 
 
 def _apart(out: torch.Tensor, what: str, **others):
@@ -74,7 +97,7 @@ def moe_route(logits, top_k, mask=None, renormalize=True, stream=None):
     divided by their sum if `renormalize`, per-expert counts, one balance loss per sequence, and
     its derivative by the probabilities, which moe_route_backward takes."""
     logits, S, T, E = _logits(logits)
-    k, lead, dev = int(top_k), tuple(logits.shape[:-2]), logits.device
+    k, lead, dev = int(top_k), logits.shape[:-2], logits.device
     if not 1 <= k <= E:
         raise ValueError(f"top_k must be in 1..{E}, got {k}")
     if mask is not None:
@@ -82,24 +105,19 @@ def moe_route(logits, top_k, mask=None, renormalize=True, stream=None):
             raise TypeError("mask must be a contiguous CUDA bool tensor")
         _shaped(mask, logits.shape[:-1], "mask")
         _same_device_as(logits, mask=mask)
-    with _on(dev, stream) as handle:
-        ids = torch.empty(logits.shape[:-1] + (k,), dtype=torch.int32, device=dev)
-        weights = torch.empty(ids.shape, dtype=torch.float32, device=dev)
-        counts = torch.empty(lead + (E,), dtype=torch.int32, device=dev)
-        loss = torch.empty(lead, dtype=torch.float32, device=dev)
-        slope = torch.empty(lead + (E,), dtype=torch.float32, device=dev)
-        scratch = torch.empty(_lib.fg_moe_route_scratch_bytes(S, T, E), dtype=torch.uint8, device=dev)
-        _check(_lib.fg_moe_route(logits.data_ptr(), DTYPES[logits.dtype], _ptr(mask), ids.data_ptr(),
-                                 weights.data_ptr(), counts.data_ptr(), loss.data_ptr(), slope.data_ptr(), S, T, E, k,
-                                 1 if renormalize else 0, scratch.data_ptr(), scratch.numel(), handle),
-               "fg_moe_route")
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, moe_route, logits, k, mask, renormalize)
+    ids = torch.empty(logits.shape[:-1] + (k,), dtype=torch.int32, device=dev)
+    weights = torch.empty_like(ids, dtype=torch.float32)
+    counts = torch.empty(lead + (E,), dtype=torch.int32, device=dev)
+    slope = torch.empty_like(counts, dtype=torch.float32)
+    loss = torch.empty(lead, dtype=torch.float32, device=dev)
+    size = _lib.fg_moe_route_scratch_bytes(S, T, E)
+    scratch, at = _scratch(size, dev)
+    _check(_lib.fg_moe_route(logits.data_ptr(), DTYPES[logits.dtype], _ptr(mask), ids.data_ptr(), weights.data_ptr(),
+                             counts.data_ptr(), loss.data_ptr(), slope.data_ptr(), S, T, E, k, 1 if renormalize else 0,
+                             at, size, _raw_stream(dev.index)), "fg_moe_route")
     return ids, weights, counts, loss, slope
-
-
-def _same_device_as(first, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, the first operand on {first.device}")
 
 
 def moe_route_backward(logits, ids, slope, grad_weights=None, grad_loss=None, renormalize=True, stream=None):
@@ -108,7 +126,7 @@ def moe_route_backward(logits, ids, slope, grad_weights=None, grad_loss=None, re
     `renormalize` must be the same.  Zeros for tokens that were not routed."""
     logits, S, T, E = _logits(logits)
     ids, slope, dev = _i32(ids, "ids"), _f32(slope, "slope"), logits.device
-    if tuple(ids.shape[:-1]) != tuple(logits.shape[:-1]) or ids.dim() != logits.dim():
+    if ids.dim() != logits.dim() or ids.shape[:-1] != logits.shape[:-1]:
         raise ValueError("ids must be [..., k] beside logits [..., E]")
     _shaped(slope, logits.shape[:-2] + (E,), "slope")
     if grad_weights is not None:
@@ -116,11 +134,12 @@ def moe_route_backward(logits, ids, slope, grad_weights=None, grad_loss=None, re
     if grad_loss is not None:
         _shaped(_f32(grad_loss, "grad_loss"), logits.shape[:-2], "grad_loss")
     _same_device_as(logits, ids=ids, slope=slope, grad_weights=grad_weights, grad_loss=grad_loss)
-    with _on(dev, stream) as handle:
-        grad = torch.empty_like(logits)
-        _check(_lib.fg_moe_route_backward(logits.data_ptr(), DTYPES[logits.dtype], ids.data_ptr(), slope.data_ptr(),
-                                          _ptr(grad_weights), _ptr(grad_loss), grad.data_ptr(), S, T, E,
-                                          ids.shape[-1], 1 if renormalize else 0, handle), "fg_moe_route_backward")
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, moe_route_backward, logits, ids, slope, grad_weights, grad_loss, renormalize)
+    grad = torch.empty_like(logits)
+    _check(_lib.fg_moe_route_backward(logits.data_ptr(), DTYPES[logits.dtype], ids.data_ptr(), slope.data_ptr(),
+                                      _ptr(grad_weights), _ptr(grad_loss), grad.data_ptr(), S, T, E, ids.shape[-1],
+                                      1 if renormalize else 0, _raw_stream(dev.index)), "fg_moe_route_backward")
     return grad
 
 
@@ -130,17 +149,23 @@ def moe_layout_rows(pairs, num_experts) -> int:
     return int(_lib.fg_moe_layout_rows(int(pairs), int(num_experts)))
 
 
-def _layout(ids, num_experts, stream, size, call):
-    ids, E = _i32(ids, "ids"), int(num_experts)
-    if not 1 <= E <= MAX_EXPERTS:
-        raise ValueError(f"num_experts must be in 1..{MAX_EXPERTS}, got {E}")
-    dev, pairs = ids.device, ids.numel()
-    with _on(dev, stream) as handle:
-        rows = torch.empty_like(ids)
-        group = torch.empty(size(pairs, E), dtype=torch.int32, device=dev)
-        scratch = torch.empty(_lib.fg_moe_layout_scratch_bytes(pairs, E), dtype=torch.uint8, device=dev)
-        call(ids.data_ptr(), rows.data_ptr(), group, pairs, E, scratch.data_ptr(), scratch.numel(), handle)
+def _layout(ids, num_experts, mmax):
+    """moe_layout_contiguous (mmax = 0) and moe_layout_masked on the current device and stream."""
+    E, pairs = int(num_experts), ids.numel()
+    rows = torch.empty_like(ids)
+    size = _lib.fg_moe_layout_scratch_bytes(pairs, E)
+    scratch, at = _scratch(size, ids.device)
+    n = E if mmax else _lib.fg_moe_layout_rows(pairs, E)
+    group = torch.empty(n, dtype=torch.int32, device=ids.device)
+    call = _lib.fg_moe_layout_masked if mmax else _lib.fg_moe_layout_contiguous
+    _check(call(ids.data_ptr(), rows.data_ptr(), group.data_ptr(), pairs, E, mmax or n, at, size,
+                _raw_stream(ids.device.index)), "fg_moe_layout_masked" if mmax else "fg_moe_layout_contiguous")
     return rows, group
+
+
+def _experts(num_experts):
+    if not 1 <= num_experts <= MAX_EXPERTS:
+        raise ValueError(f"num_experts must be in 1..{MAX_EXPERTS}, got {num_experts}")
 
 
 def moe_layout_contiguous(ids, num_experts, stream=None):
@@ -148,9 +173,11 @@ def moe_layout_contiguous(ids, num_experts, stream=None):
     expert, any value outside [0, num_experts) = none.  Returns (rows int32 like ids, -1 for none;
     m_indices int32 [M]) with M = moe_layout_rows(ids.numel(), num_experts), which no choice exceeds;
     an expert's rows are in the order of ids."""
-    return _layout(ids, num_experts, stream, moe_layout_rows,
-                   lambda i, r, group, n, E, ws, size, s: _check(_lib.fg_moe_layout_contiguous(
-                       i, r, group.data_ptr(), n, E, group.numel(), ws, size, s), "fg_moe_layout_contiguous"))
+    ids = _i32(ids, "ids")
+    _experts(num_experts)
+    if _elsewhere(ids.device, stream):
+        return _there(ids.device, stream, _layout, ids, num_experts, 0)
+    return _layout(ids, num_experts, 0)
 
 
 def moe_layout_masked(ids, num_experts, mmax, stream=None):
@@ -159,9 +186,11 @@ def moe_layout_masked(ids, num_experts, mmax, stream=None):
     mmax = int(mmax)
     if mmax < 1:
         raise ValueError(f"mmax must be positive, got {mmax}")
-    return _layout(ids, num_experts, stream, lambda n, E: E,
-                   lambda i, r, group, n, E, ws, size, s: _check(_lib.fg_moe_layout_masked(
-                       i, r, group.data_ptr(), n, E, mmax, ws, size, s), "fg_moe_layout_masked"))
+    ids = _i32(ids, "ids")
+    _experts(num_experts)
+    if _elsewhere(ids.device, stream):
+        return _there(ids.device, stream, _layout, ids, num_experts, mmax)
+    return _layout(ids, num_experts, mmax)
 
 
 def _rows(rows, tokens):
@@ -186,25 +215,25 @@ def moe_dispatch_fp8(x, rows, shape=None, A=None, sfa=None, fmt="e4m3", stream=N
     if A is not None:
         if A.dtype != torch.uint8 or not A.is_cuda or not A.is_contiguous() or A.dim() not in (2, 3):
             raise ValueError("A must be a contiguous CUDA uint8 tensor [M, K] or [G, Mmax, K]")
-        if shape is not None and tuple(A.shape[:-1]) != _lead(shape):
+        if shape is not None and A.shape[:-1] != _lead(shape):
             raise ValueError("A does not have the given shape")
-        shape = tuple(A.shape[:-1])
+        shape = A.shape[:-1]
     shape = _lead(shape)
-    G, M = (1,) * (2 - len(shape)) + shape
-    scales = shape[:-1] + (_cdiv(K, 128), sfa_ld(M))
+    G, M = shape if len(shape) == 2 else (1, *shape)
+    scales = shape[:-1] + (_cdiv(K, 128), (M + 3) // 4 * 4)
+    _same_device_as(x, rows=rows, A=A, sfa=sfa)
     if A is not None:
         _shaped(A, shape + (K,), "A")
         _shaped(_f32(sfa, "sfa"), scales, "sfa")
-    _same_device(dev, rows=rows, **({} if A is None else dict(A=A, sfa=sfa)))
-    with _on(dev, stream) as handle:
-        if A is None:
-            A = torch.empty(shape + (K,), dtype=torch.uint8, device=dev)
-            sfa = torch.zeros(scales, dtype=torch.float32, device=dev)
-        else:
-            _apart(A, "A", x=x, rows=rows, sfa=sfa)
-            _apart(sfa, "sfa", x=x, rows=rows)
-        _check(_lib.fg_moe_dispatch_fp8(x.data_ptr(), rows.data_ptr(), A.data_ptr(), sfa.data_ptr(), T,
-                                        rows.shape[1], G, M, K, FORMATS[fmt], handle), "fg_moe_dispatch_fp8")
+        _apart(A, "A", x=x, rows=rows, sfa=sfa)
+        _apart(sfa, "sfa", x=x, rows=rows)
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, moe_dispatch_fp8, x, rows, shape, A, sfa, fmt)
+    if A is None:
+        A = torch.empty(shape + (K,), dtype=torch.uint8, device=dev)
+        sfa = torch.zeros(scales, dtype=torch.float32, device=dev)
+    _check(_lib.fg_moe_dispatch_fp8(x.data_ptr(), rows.data_ptr(), A.data_ptr(), sfa.data_ptr(), T, rows.shape[1], G,
+                                    M, K, FORMATS[fmt], _raw_stream(dev.index)), "fg_moe_dispatch_fp8")
     return A, sfa
 
 
@@ -236,11 +265,12 @@ def moe_combine(C, rows, weights=None, out=None, stream=None):
     if out is not None:
         _shaped(_bf16(out, "out"), (T, N), "out")
         _apart(out, "out", C=C, rows=rows, weights=weights)
-    with _on(dev, stream) as handle:
-        if out is None:
-            out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
-        _check(_lib.fg_moe_combine(C.data_ptr(), rows.data_ptr(), _ptr(weights), out.data_ptr(), T, k, M, N, handle),
-               "fg_moe_combine")
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, moe_combine, C, rows, weights, out)
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+    _check(_lib.fg_moe_combine(C.data_ptr(), rows.data_ptr(), _ptr(weights), out.data_ptr(), T, k, M, N,
+                               _raw_stream(dev.index)), "fg_moe_combine")
     return out
 
 
@@ -256,13 +286,14 @@ def moe_combine_backward(grad_out, C, rows, weights, grad_C=None, stream=None):
     if grad_C is not None:
         _shaped(_bf16(grad_C, "grad_C"), C.shape, "grad_C")
         _apart(grad_C, "grad_C", C=C, grad_out=grad_out, rows=rows, weights=weights)
-    with _on(dev, stream) as handle:
-        if grad_C is None:
-            grad_C = torch.empty_like(C)
-        grad_weights = torch.empty(rows.shape, dtype=torch.float32, device=dev)
-        _check(_lib.fg_moe_combine_backward(grad_out.data_ptr(), C.data_ptr(), rows.data_ptr(), weights.data_ptr(),
-                                            grad_C.data_ptr(), grad_weights.data_ptr(), T, k, M, N, handle),
-               "fg_moe_combine_backward")
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, moe_combine_backward, grad_out, C, rows, weights, grad_C)
+    if grad_C is None:
+        grad_C = torch.empty_like(C)
+    grad_weights = torch.empty_like(rows, dtype=torch.float32)
+    _check(_lib.fg_moe_combine_backward(grad_out.data_ptr(), C.data_ptr(), rows.data_ptr(), weights.data_ptr(),
+                                        grad_C.data_ptr(), grad_weights.data_ptr(), T, k, M, N,
+                                        _raw_stream(dev.index)), "fg_moe_combine_backward")
     return grad_C, grad_weights
 
 
@@ -288,9 +319,10 @@ def lora_add(C, x, lora_a, lora_b, adapters, scaling=None, out=None, stream=None
         if out.data_ptr() != C.data_ptr():
             _apart(out, "out", C=C)
         _apart(out, "out", x=x, lora_a=lora_a, lora_b=lora_b, adapters=adapters, scaling=scaling)
-    with _on(dev, stream) as handle:
-        if out is None:
-            out = torch.empty_like(C)
-        _check(_lib.fg_lora_add(C.data_ptr(), x.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(), adapters.data_ptr(),
-                                _ptr(scaling), out.data_ptr(), M, N, K, R, L, handle), "fg_lora_add")
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, lora_add, C, x, lora_a, lora_b, adapters, scaling, out)
+    if out is None:
+        out = torch.empty_like(C)
+    _check(_lib.fg_lora_add(C.data_ptr(), x.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(), adapters.data_ptr(),
+                            _ptr(scaling), out.data_ptr(), M, N, K, R, L, _raw_stream(dev.index)), "fg_lora_add")
     return out

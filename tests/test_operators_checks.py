@@ -31,7 +31,7 @@ def test_layout_rows_hold_every_choice():
 
 @pytest.mark.parametrize("change,expect", [
     (dict(), None), (dict(logits=NULL), 1), (dict(ids=NULL), 1), (dict(weights=NULL), 1), (dict(counts=NULL), 1),
-    (dict(loss=NULL), 1), (dict(slope=NULL), 1), (dict(scratch=NULL), 1), (dict(dtype=3), 1), (dict(S=-1), 1),
+    (dict(loss=NULL), 1), (dict(slope=NULL), 1), (dict(dtype=3), 1), (dict(S=-1), 1),
     (dict(T=-1), 1), (dict(E=0), 1), (dict(k=0), 1), (dict(k=9), 1), (dict(E=1025), 3), (dict(E=64, k=33), 3),
     (dict(S=65536), 3), (dict(logits=P + 2), 2), (dict(ids=P + 2), 2), (dict(S=0), 0),
 ])
