@@ -127,8 +127,13 @@ def _declare(l: ctypes.CDLL) -> ctypes.CDLL:
     l.fg_moe_combine.restype = _int
     l.fg_moe_combine_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _int, _int, _int, _int, _vp]
     l.fg_moe_combine_backward.restype = _int
-    l.fg_lora_add.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _int, _int, _int, _int, _int, _vp]
+    l.fg_lora_scratch_bytes.argtypes = [_int, _int]
+    l.fg_lora_scratch_bytes.restype = ctypes.c_size_t
+    l.fg_lora_add.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _int, _int, _int, _int, _int, _vp, ctypes.c_size_t,
+                              _vp]
     l.fg_lora_add.restype = _int
+    l.fg_lora_status.argtypes = [_vp]
+    l.fg_lora_status.restype = _int
     l.fg_launch_count.argtypes = []
     l.fg_launch_count.restype = ctypes.c_uint64
     return l
@@ -465,5 +470,5 @@ def cast_fp8_blocks(w, stream=None, fmt="e4m3"):
 
 # ---------------------------------------------------------------------------- around the GEMMs
 from .operators import (  # noqa: E402
-    lora_add, moe_combine, moe_combine_backward, moe_dispatch_fp8, moe_layout_contiguous, moe_layout_masked,
+    lora_add, lora_status, moe_combine, moe_combine_backward, moe_dispatch_fp8, moe_layout_contiguous, moe_layout_masked,
     moe_layout_rows, moe_route, moe_route_backward)

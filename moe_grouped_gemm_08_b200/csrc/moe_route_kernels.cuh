@@ -24,12 +24,17 @@ constexpr int kRouteMaxK = 32;
 constexpr int kRouteMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ uint32_t bits_of(float v) { return __float_as_uint(v); }
-__device__ __forceinline__ uint32_t bits_of(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
-__device__ __forceinline__ uint32_t bits_of(__half v) { return __half_as_ushort(v); }
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <typename T>
+struct IsHalf {
+  static constexpr bool value = false;
+};
+template <>
+struct IsHalf<__half> {
+  static constexpr bool value = true;
+};
 template <typename T>
 __device__ __forceinline__ T from_f32(float v);
 template <>
@@ -39,40 +44,36 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { retu
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-// Orders a row's choices: a larger key is an earlier choice.  The upper part is the logit's bits made
-// monotonic, the lower one counts columns down, so that equal logits come lowest expert first; 0 for
-// logits that are never chosen (-inf, NaN, no column).  16-bit logits share one 32-bit word with
-// their column, which one warp reduction orders; fp32 logits take 64 bits and two.
+// Orders a row's choices: a larger key is an earlier choice.  The upper part is the logit's fp32 bits made
+// monotonic, the lower ten bits count columns down, so that equal logits come lowest expert first.  bf16
+// and fp16 values have no fp32 bits below the 13th, so the key is one 32-bit word, which one warp
+// reduction orders; fp32 logits take 64 bits and two reductions.  -0 and +0 are equal; -inf and NaN,
+// which are never chosen, have keys below kClosed.
 template <typename T>
 struct RouteKey {
   typedef uint32_t type;
-  static __device__ __forceinline__ type make(T v, float f, int col) {
-    uint32_t u = bits_of(v);
-    if (u == 0x8000u) u = 0;  // -0 and +0 are equal
-    u = (u & 0x8000u) ? (~u & 0xFFFFu) : (u | 0x8000u);
-    return f > -INFINITY ? (u << 16) | static_cast<uint32_t>(0xFFFF - col) : 0u;
+  static constexpr type kClosed = 0x00800000u;  // keys of -inf: 0x007FFC00 + column
+  static __device__ __forceinline__ type make(float v, int inverse_col) {
+    const uint32_t u = __float_as_uint(fmaxf(v + 0.0f, -INFINITY));
+    return ((u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u)) & 0xFFFFFC00u) |
+           static_cast<uint32_t>(inverse_col);
   }
-  static __device__ __forceinline__ int col(type k) { return 0xFFFF - static_cast<int>(k & 0xFFFFu); }
+  static __device__ __forceinline__ int col(type k) { return 1023 - static_cast<int>(k & 1023u); }
   static __device__ __forceinline__ float logit(type k) {
-    const uint32_t u = k >> 16;
-    const unsigned short h = static_cast<unsigned short>((u & 0x8000u) ? (u & 0x7FFFu) : (~u & 0xFFFFu));
-    if constexpr (sizeof(T) == 2) {
-      T t;
-      memcpy(&t, &h, 2);
-      return to_f32(t);
-    }
-    return 0.0f;
+    const uint32_t u = k & 0xFFFFFC00u;
+    return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u & 0xFFFFFC00u);
   }
 };
 template <>
 struct RouteKey<float> {
   typedef unsigned long long type;
-  static __device__ __forceinline__ type make(float v, float, int col) {
-    const uint32_t u = __float_as_uint(v + 0.0f);  // -0 and +0 are equal
-    const uint32_t key = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    return v > -INFINITY ? (static_cast<type>(key) << 32) | static_cast<uint32_t>(0xFFFF - col) : 0ull;
+  static constexpr type kClosed = 0x0080000000000000ull;
+  static __device__ __forceinline__ type make(float v, int inverse_col) {
+    const uint32_t u = __float_as_uint(fmaxf(v + 0.0f, -INFINITY));
+    const uint32_t key = u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u);
+    return (static_cast<type>(key) << 32) | static_cast<uint32_t>(inverse_col);
   }
-  static __device__ __forceinline__ int col(type k) { return 0xFFFF - static_cast<int>(k & 0xFFFFu); }
+  static __device__ __forceinline__ int col(type k) { return 1023 - static_cast<int>(k & 1023u); }
   static __device__ __forceinline__ float logit(type k) {
     const uint32_t u = static_cast<uint32_t>(k >> 32);
     return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
@@ -189,7 +190,7 @@ __device__ __forceinline__ void load_logits(const T* row, int E, int sub, T (&x)
       if (c < E) {
         raw = *reinterpret_cast<const uint4*>(row + c);
       } else {
-        const uint32_t none = sizeof(T) == 4 ? 0xFF800000u : bits_of(from_f32<T>(-INFINITY)) * 0x10001u;
+        const uint32_t none = sizeof(T) == 4 ? 0xFF800000u : IsHalf<T>::value ? 0xFC00FC00u : 0xFF80FF80u;
         raw = make_uint4(none, none, none, none);
       }
       memcpy(&x[i], &raw, 16);
@@ -264,31 +265,34 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
   const int first = chunk * p.rows_per_chunk;
   const int last = min(p.T, first + p.rows_per_chunk);
   const size_t base = static_cast<size_t>(seq) * p.T;
-  const T* logits = static_cast<const T*>(p.logits);
+  const T* logits = static_cast<const T*>(p.logits) + base * p.E;
+  const uint8_t* mask = p.mask ? p.mask + base : nullptr;
+  int* ids = p.ids + base * p.k;
+  float* weights = p.weights + base * p.k;
   T next[NPL];
   bool next_live = false;
   auto fetch = [&](int r0) {  // rows behind the last one repeat it and are dropped later
     const int r = min(r0 + rw, last - 1);
-    next_live = !p.mask || p.mask[base + r];
-    load_logits<T, LPR, NPL, V>(logits + (base + r) * p.E, p.E, sub, next);
+    next_live = !mask || mask[r];
+    load_logits<T, LPR, NPL, V>(logits + static_cast<size_t>(r) * p.E, p.E, sub, next);
   };
+  K* keys = s_key[warp][rw];
   int r0 = first + warp * RPW;
   if (r0 < last) fetch(r0);
   for (; r0 < last; r0 += kRouteWarps * RPW) {
     const int r = r0 + rw;
-    const size_t row = base + r;
     const bool live = r < last && next_live;
     float x[NPL];
     K key[NPL];
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
       x[i] = to_f32(next[i]);
-      key[i] = live ? Key::make(next[i], x[i], route_col<LPR, V>(i, sub)) : K(0);
+      key[i] = Key::make(x[i], 1023 - route_col<LPR, V>(i, sub));
     }
     if (r0 + kRouteWarps * RPW < last) fetch(r0 + kRouteWarps * RPW);
     sort_falling<0, NPL>(key);
     K best = row_best<LPR>(key[0]);
-    const bool routed = best != 0;
+    const bool routed = live && best >= Key::kClosed;
     const float high = routed ? Key::logit(best) : 0.0f;
     float sum = 0.0f;
 #pragma unroll
@@ -297,19 +301,24 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
       sum += x[i];
     }
     for (int j = 0; j < p.k; ++j) {
-      if (sub == j % LPR) s_key[warp][rw][j] = best;
-      if (key[0] == best) {
+      if (key[0] == best) {  // the winner's lane (keys differ by their columns; 0 once a list is empty)
+        keys[j] = best;
 #pragma unroll
         for (int i = 0; i + 1 < NPL; ++i) key[i] = key[i + 1];
         key[NPL - 1] = 0;
       }
-      if (j + 1 < p.k) best = row_best<LPR>(key[0]);
+      best = row_best<LPR>(key[0]);
     }
     __syncwarp();
     float sums[2] = {sum, 0.0f};  // over all columns; over the choices
-    for (int j = sub; j < p.k; j += LPR) {
-      const K c = s_key[warp][rw][j];
-      if (c) sums[1] += softmax_exp(Key::logit(c), high);
+    K choice = 0;
+    if (sub < p.k && routed) choice = keys[sub];
+    float u = choice >= Key::kClosed ? softmax_exp(Key::logit(choice), high) : 0.0f;
+    sums[1] = u;
+    if constexpr (LPR < kRouteMaxK) {
+      if (routed)
+        for (int j = sub + LPR; j < p.k; j += LPR)
+          if (keys[j] >= Key::kClosed) sums[1] += softmax_exp(Key::logit(keys[j]), high);
     }
     row_sums<LPR>(sums);
     const float inv = 1.0f / sums[0];
@@ -319,11 +328,19 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
     }
     if (r < last) {
       const float scale = p.renorm ? 1.0f / sums[1] : inv;
-      for (int j = sub; j < p.k; j += LPR) {
-        const K c = s_key[warp][rw][j];
-        p.ids[row * p.k + j] = c ? Key::col(c) : -1;
-        p.weights[row * p.k + j] = c ? softmax_exp(Key::logit(c), high) * scale : 0.0f;
-        if (c) atomicAdd(&s_cnt[Key::col(c)], 1);
+      auto put = [&](int j, K c, float w) {
+        const bool chosen = c >= Key::kClosed;
+        const size_t at = static_cast<size_t>(r) * p.k + j;
+        ids[at] = chosen ? Key::col(c) : -1;
+        weights[at] = chosen ? w * scale : 0.0f;
+        if (chosen) atomicAdd(&s_cnt[Key::col(c)], 1);
+      };
+      if (sub < p.k) put(sub, choice, u);
+      if constexpr (LPR < kRouteMaxK) {
+        for (int j = sub + LPR; j < p.k; j += LPR) {
+          choice = routed ? keys[j] : K(0);
+          put(j, choice, choice >= Key::kClosed ? softmax_exp(Key::logit(choice), high) : 0.0f);
+        }
       }
       if (sub == 0 && routed) atomicAdd(&s_cnt[EP], 1);
     }
@@ -453,27 +470,29 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_backward_kernel(const
   const int first = blockIdx.x * p.rows_per_chunk;
   const int last = min(p.T, first + p.rows_per_chunk);
   const size_t base = static_cast<size_t>(seq) * p.T;
-  const T* all = static_cast<const T*>(p.logits);
+  const T* all = static_cast<const T*>(p.logits) + base * p.E;
+  T* out_all = static_cast<T*>(p.grad_logits) + base * p.E;
+  const int* ids = p.ids + base * p.k;
+  const float* weights = p.grad_weights ? p.grad_weights + base * p.k : nullptr;
   T next[NPL];
   int next_id = -1;
   float next_g = 0.0f;
-  auto choice = [&](size_t row, int j, int& id, float& gw) {
-    id = p.ids[row * p.k + j];
-    if (id < 0 || id >= p.E) id = -1;
-    gw = p.grad_weights && id >= 0 ? p.grad_weights[row * p.k + j] : 0.0f;
+  auto choice = [&](int r, int j, int& id, float& gw) {
+    const size_t at = static_cast<size_t>(r) * p.k + j;
+    id = ids[at];
+    if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.E)) id = -1;
+    gw = weights ? weights[at] : 0.0f;
   };
   auto fetch = [&](int r0) {
-    const size_t row = base + min(r0 + rw, last - 1);
-    load_logits<T, LPR, NPL, V>(all + row * p.E, p.E, sub, next);
-    next_id = -1;
-    if (sub < p.k) choice(row, sub, next_id, next_g);
+    const int r = min(r0 + rw, last - 1);
+    load_logits<T, LPR, NPL, V>(all + static_cast<size_t>(r) * p.E, p.E, sub, next);
+    if (sub < p.k) choice(r, sub, next_id, next_g);
   };
   int r0 = first + warp * RPW;
   if (r0 < last) fetch(r0);
   for (; r0 < last; r0 += kRouteWarps * RPW) {
-    const int r = r0 + rw;
-    const size_t row = base + min(r, last - 1);
-    const T* logits = all + row * p.E;
+    const int r = min(r0 + rw, last - 1);
+    const T* logits = all + static_cast<size_t>(r) * p.E;
     float x[NPL];
     float m = -INFINITY;
 #pragma unroll
@@ -484,6 +503,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_backward_kernel(const
     const int id = next_id;
     const float gw = next_g;
     if (r0 + kRouteWarps * RPW < last) fetch(r0 + kRouteWarps * RPW);
+    const float chosen = id >= 0 ? to_f32(logits[id]) : 0.0f;  // the row's own: in L1
     const float high = row_max<LPR>(m);
     // sums of u, of u h, of u over the choices, of u g over the choices
     float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -494,18 +514,20 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_backward_kernel(const
       sums[1] = fmaf(x[i], h[i], sums[1]);
     }
     bool any = id >= 0;
-    const float u = id >= 0 ? softmax_exp(to_f32(logits[id]), high) : 0.0f;
+    const float u = id >= 0 ? softmax_exp(chosen, high) : 0.0f;
     sums[2] = u;
-    sums[3] = u * gw;
-    for (int j = sub + LPR; j < p.k; j += LPR) {
-      int id2;
-      float gw2;
-      choice(row, j, id2, gw2);
-      if (id2 < 0) continue;
-      any = true;
-      const float u2 = softmax_exp(to_f32(logits[id2]), high);
-      sums[2] += u2;
-      sums[3] = fmaf(u2, gw2, sums[3]);
+    sums[3] = id >= 0 ? u * gw : 0.0f;
+    if constexpr (LPR < kRouteMaxK) {
+      for (int j = sub + LPR; j < p.k; j += LPR) {
+        int id2;
+        float gw2;
+        choice(r, j, id2, gw2);
+        if (id2 < 0) continue;
+        any = true;
+        const float u2 = softmax_exp(to_f32(logits[id2]), high);
+        sums[2] += u2;
+        sums[3] = fmaf(u2, gw2, sums[3]);
+      }
     }
     const uint32_t votes = __ballot_sync(0xffffffffu, any);
     const bool routed = (votes >> (rw * LPR)) & (LPR == 32 ? 0xffffffffu : (1u << (LPR & 31)) - 1);
@@ -514,22 +536,25 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_backward_kernel(const
     const float top = p.renorm ? 1.0f / sums[2] : inv;
     const float mean = p.renorm ? sums[3] * top : 0.0f;
     const float dot = (p.renorm ? sums[1] : sums[1] + sums[3]) * inv;
-    if (p.grad_weights) {  // shared atomics: a choice may stand twice
+    if (weights) {  // shared atomics: a choice may stand twice
       if (id >= 0) atomicAdd(&add[id], u * top * (gw - mean));
-      for (int j = sub + LPR; j < p.k; j += LPR) {
-        int id2;
-        float gw2;
-        choice(row, j, id2, gw2);
-        if (id2 >= 0) atomicAdd(&add[id2], softmax_exp(to_f32(logits[id2]), high) * top * (gw2 - mean));
+      if constexpr (LPR < kRouteMaxK) {
+        for (int j = sub + LPR; j < p.k; j += LPR) {
+          int id2;
+          float gw2;
+          choice(r, j, id2, gw2);
+          if (id2 >= 0) atomicAdd(&add[id2], softmax_exp(to_f32(logits[id2]), high) * top * (gw2 - mean));
+        }
       }
       __syncwarp();
     }
-    T* out = static_cast<T*>(p.grad_logits) + row * p.E;
+    T* out = out_all + static_cast<size_t>(r) * p.E;
+    const bool write = r0 + rw < last;
 #pragma unroll
     for (int i = 0; i < NPL; i += V) {
       const int c = route_col<LPR, V>(i, sub);
       alignas(16) T t[V];
-      float a[V];
+      alignas(16) float a[V];
       if constexpr (V % 4 == 0) {
 #pragma unroll
         for (int v = 0; v < V; v += 4) *reinterpret_cast<float4*>(a + v) = *reinterpret_cast<const float4*>(add + c + v);
@@ -538,21 +563,23 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_backward_kernel(const
       }
 #pragma unroll
       for (int v = 0; v < V; ++v) t[v] = from_f32<T>(routed ? fmaf(x[i + v] * inv, h[i + v] - dot, a[v]) : 0.0f);
-      if (c < p.E && r < last) {
+      if (c < p.E && write) {
         if constexpr (V == 1)
           out[c] = t[0];
         else
           *reinterpret_cast<uint4*>(out + c) = *reinterpret_cast<const uint4*>(t);
       }
     }
-    if (p.grad_weights) {
+    if (weights) {
       __syncwarp();
       if (id >= 0) add[id] = 0.0f;
-      for (int j = sub + LPR; j < p.k; j += LPR) {
-        int id2;
-        float gw2;
-        choice(row, j, id2, gw2);
-        if (id2 >= 0) add[id2] = 0.0f;
+      if constexpr (LPR < kRouteMaxK) {
+        for (int j = sub + LPR; j < p.k; j += LPR) {
+          int id2;
+          float gw2;
+          choice(r, j, id2, gw2);
+          if (id2 >= 0) add[id2] = 0.0f;
+        }
       }
       __syncwarp();
     }

@@ -15,8 +15,6 @@ namespace fg {
 
 constexpr int kLayoutThreads = 256;
 constexpr int kLayoutWarps = kLayoutThreads / 32;
-constexpr int kLayoutItems = 8;                               // pairs per thread
-constexpr int kLayoutChunk = kLayoutThreads * kLayoutItems;   // pairs per CTA
 constexpr int kLayoutMaxExperts = 1024;
 constexpr int kRowsMaxK = 32;
 
@@ -27,21 +25,30 @@ struct LayoutParams {
   int* hist;       // [chunks][E], unused with one chunk
   long long pairs;
   int E, chunks, M, mmax, align;  // mmax > 0: masked layout
+  int* inverse;  // [M], the pair of each occupied row; nullptr: not wanted (then rows is)
+  int rest;      // 1: ids outside [0, E - 1) are expert E - 1; 0: they have no row
 };
 
-// Counts per expert of one chunk of pairs.
+__device__ __forceinline__ int layout_id(const LayoutParams& p, long long at) {
+  if (at >= p.pairs) return -1;
+  const int id = p.ids[at], none = p.rest ? p.E - 1 : -1;
+  return id >= 0 && id < p.E - p.rest ? id : none;
+}
+
+// Counts per expert of one chunk of pairs (kLayoutThreads * ITEMS, in their order).
+template <int ITEMS>
 __global__ void __launch_bounds__(kLayoutThreads) moe_layout_count_kernel(const LayoutParams p) {
   __shared__ int s_cnt[kLayoutMaxExperts];
   for (int e = threadIdx.x; e < p.E; e += kLayoutThreads) s_cnt[e] = 0;
   __syncthreads();
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  const long long base = static_cast<long long>(blockIdx.x) * kLayoutChunk;
+  const long long base = static_cast<long long>(blockIdx.x) * (kLayoutThreads * ITEMS);
 #pragma unroll
-  for (int i = 0; i < kLayoutItems; ++i) {
+  for (int i = 0; i < ITEMS; ++i) {
     const long long at = base + i * kLayoutThreads + threadIdx.x;
-    const int id = at < p.pairs ? p.ids[at] : -1;
-    if (id >= 0 && id < p.E) atomicAdd(&s_cnt[id], 1);
+    const int id = layout_id(p, at);
+    if (id >= 0) atomicAdd(&s_cnt[id], 1);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < p.E; e += kLayoutThreads)
@@ -50,28 +57,48 @@ __global__ void __launch_bounds__(kLayoutThreads) moe_layout_count_kernel(const 
 
 // The stable counting sort of a chunk: a pair's row is its expert's first row, plus the expert's
 // pairs in earlier chunks, in earlier warps of the chunk, and earlier in its warp.
+template <int ITEMS>
 __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(const LayoutParams p) {
   __shared__ uint16_t s_warp[kLayoutWarps][kLayoutMaxExperts];  // counts, then prefixes over the warps
-  __shared__ int s_start[kLayoutMaxExperts];  // the expert's first row
-  __shared__ int s_count[kLayoutMaxExperts];  // its pairs
+  __shared__ int s_start[kLayoutMaxExperts];   // the expert's first row
+  __shared__ int s_count[kLayoutMaxExperts];   // its pairs
   __shared__ int s_before[kLayoutMaxExperts];  // its pairs in earlier chunks
   __shared__ int s_scan[kLayoutWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < kLayoutWarps * kLayoutMaxExperts; i += kLayoutThreads) (&s_warp[0][0])[i] = 0;
+  for (int e = threadIdx.x; e < p.E; e += kLayoutThreads) {
+#pragma unroll
+    for (int w = 0; w < kLayoutWarps; ++w) s_warp[w][e] = 0;
+    s_before[e] = 0;
+    s_count[e] = 0;
+  }
   __syncthreads();
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  const long long base = static_cast<long long>(blockIdx.x) * kLayoutChunk + warp * 32 * kLayoutItems;
-  int id[kLayoutItems], rank[kLayoutItems];
+  const long long base = static_cast<long long>(blockIdx.x) * (kLayoutThreads * ITEMS) + warp * 32 * ITEMS;
+  int id[ITEMS], rank[ITEMS];
 #pragma unroll
-  for (int i = 0; i < kLayoutItems; ++i) {
-    const long long at = base + i * 32 + lane;
-    id[i] = at < p.pairs ? p.ids[at] : -1;
-    if (id[i] >= p.E) id[i] = -1;
+  for (int i = 0; i < ITEMS; ++i) {
+    id[i] = layout_id(p, base + i * 32 + lane);
+  }
+  if (p.chunks > 1) {  // all threads over (chunk, expert), as many chunks side by side as there is room
+    const int cols = p.E < 32 ? 32 : p.E < kLayoutThreads ? (p.E + 31) / 32 * 32 : kLayoutThreads;
+    const int parts = kLayoutThreads / cols;
+    const int part = threadIdx.x / cols;
+    for (int e = threadIdx.x % cols; e < p.E && part < parts; e += cols) {
+      int before = 0, count = 0;
+#pragma unroll 8
+      for (int c = part; c < p.chunks; c += parts) {
+        const int v = p.hist[static_cast<size_t>(c) * p.E + e];
+        before += c < static_cast<int>(blockIdx.x) ? v : 0;
+        count += v;
+      }
+      atomicAdd(&s_before[e], before);
+      atomicAdd(&s_count[e], count);
+    }
   }
 #pragma unroll
-  for (int i = 0; i < kLayoutItems; ++i) {
-    const int e = id[i] < 0 ? -1 : id[i];
+  for (int i = 0; i < ITEMS; ++i) {
+    const int e = id[i];
     const uint32_t same = __match_any_sync(0xffffffffu, e);
     const int before = e >= 0 ? s_warp[warp][e] : 0;
     rank[i] = before + __popc(same & ((1u << lane) - 1));
@@ -88,17 +115,7 @@ __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(const Layout
       s_warp[w][e] = static_cast<uint16_t>(run);
       run += c;
     }
-    int before = 0, count = run;
-    if (p.chunks > 1) {
-      count = 0;
-      for (int c = 0; c < p.chunks; ++c) {
-        const int v = p.hist[static_cast<size_t>(c) * p.E + e];
-        if (c < static_cast<int>(blockIdx.x)) before += v;
-        count += v;
-      }
-    }
-    s_before[e] = before;
-    s_count[e] = count;
+    if (p.chunks <= 1) s_count[e] = run;
   }
   __syncthreads();
   // first rows: the experts' blocks one after the other, each padded to the alignment
@@ -132,7 +149,7 @@ __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(const Layout
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kLayoutItems; ++i) {
+  for (int i = 0; i < ITEMS; ++i) {
     const long long at = base + i * 32 + lane;
     if (at >= p.pairs) continue;
     const int e = id[i];
@@ -141,7 +158,10 @@ __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(const Layout
       const int place = s_before[e] + s_warp[warp][e] + rank[i];
       if (p.mmax <= 0 || place < p.mmax) row = s_start[e] + place;
     }
-    p.rows[at] = row;
+    if (p.inverse)
+      p.inverse[row] = static_cast<int>(at);  // with `rest` every pair has a row
+    else
+      p.rows[at] = row;
   }
   if (p.mmax > 0) {
     if (blockIdx.x == 0)
@@ -169,8 +189,40 @@ struct DispatchParams {
   int k, K, M, mmax, ld;   // M: all rows of the layout; mmax: rows of a group (contiguous: M)
 };
 
-// One warp per token and 1024 columns: the row is read and cast once (as fp8_cast_rows_kernel
-// does), then stored at each of its rows.
+// The FP8 codes of 16 values of one block.  The definition is the format's rounding of RN(x / scale).
+// Inside the range below, q = RN(x r), r = RN(1 / scale), corrected once by its remainder (Markstein, "Computation
+// of elementary functions on the IBM RISC System/6000", 1990) is that quotient: for x of 8 significant
+// bits and scale = RN(amax / 448) with amax of 8 bits it was checked for all 128 x 128 mantissas, and
+// scaling both by powers of two changes nothing.  (Values so small that their remainder underflows
+// are 0 in either format.)  The signs keep -0 as it is.
+template <int FMT>
+__device__ __forceinline__ uint4 encode_fp8x16(const float (&f)[16], float scale) {
+  constexpr __nv_fp8_interpretation_t kind = FMT == 0 ? __NV_E4M3 : __NV_E5M2;
+  uint32_t h[8];
+  if (scale >= 0x1p-80f) {
+    const float r = __frcp_rn(scale);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float q[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        q[j] = f[2 * i + j] * r;
+        q[j] = fmaf(-fmaf(q[j], scale, -f[2 * i + j]), r, q[j]);
+      }
+      h[i] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, kind));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      h[i] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(
+          make_float2(__fdiv_rn(f[2 * i], scale), __fdiv_rn(f[2 * i + 1], scale)), __NV_SATFINITE, kind));
+  }
+  return make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+}
+
+// One warp per token and kDispatchSpans * 512 columns, 16 per lane, so eight lanes hold a 128-wide block:
+// the row is read and cast once, then stored at each of its rows.
+constexpr int kDispatchSpans = 2;
 template <int FMT>
 __global__ void __launch_bounds__(256) moe_dispatch_kernel(const DispatchParams p, int chunks) {
   const int lane = threadIdx.x & 31;
@@ -184,38 +236,47 @@ __global__ void __launch_bounds__(256) moe_dispatch_kernel(const DispatchParams 
     const int c = static_cast<int>(w - t * chunks);
     int mine = lane < p.k ? p.rows[t * p.k + lane] : -1;
     if (mine >= p.M) mine = -1;
-    if (__ballot_sync(0xffffffffu, mine >= 0) == 0) continue;
     const __nv_bfloat16* xr = p.x + t * p.K;
-    uint4 raw[kCastSpans];
+    const int col0 = c * (kDispatchSpans * 512) + lane * 16;
+    uint4 raw[kDispatchSpans][2];
 #pragma unroll
-    for (int j = 0; j < kCastSpans; ++j) {
-      const int col = (c * kCastSpans + j) * 256 + lane * 8;
-      raw[j] = col < p.K ? __ldg(reinterpret_cast<const uint4*>(xr + col)) : make_uint4(0u, 0u, 0u, 0u);
+    for (int j = 0; j < kDispatchSpans; ++j) {
+      const int col = col0 + j * 512;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        raw[j][h] = col < p.K ? __ldg(reinterpret_cast<const uint4*>(xr + col) + h) : make_uint4(0u, 0u, 0u, 0u);
     }
-    uint2 code[kCastSpans];
-    float scale[kCastSpans];
+    uint32_t left = __ballot_sync(0xffffffffu, mine >= 0);
+    if (left == 0) continue;
+    uint4 code[kDispatchSpans];
+    float scale[kDispatchSpans];
 #pragma unroll
-    for (int j = 0; j < kCastSpans; ++j) {
-      float f[8];
-      unpack_bf16x8(raw[j], f);
+    for (int j = 0; j < kDispatchSpans; ++j) {
+      float lo[8], hi[8], f[16];
+      unpack_bf16x8(raw[j][0], lo);
+      unpack_bf16x8(raw[j][1], hi);
       float amax = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
+      for (int i = 0; i < 8; ++i) {
+        f[i] = lo[i];
+        f[8 + i] = hi[i];
+        amax = fmaxf(amax, fmaxf(fabsf(lo[i]), fabsf(hi[i])));
+      }
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       scale[j] = cast_scale<FMT>(amax);
-      code[j] = encode_fp8x8<FMT>(f, scale[j]);
+      code[j] = encode_fp8x16<FMT>(f, scale[j]);
     }
-    for (int q = 0; q < p.k; ++q) {
-      const int row = __shfl_sync(0xffffffffu, mine, q);
-      if (row < 0) continue;
+    for (; left; left &= left - 1) {
+      const int row = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1);
       const int g = row / p.mmax, m = row - g * p.mmax;
+      uint8_t* dst = p.A + static_cast<size_t>(row) * p.K + col0;
+      float* sdst = p.sfa + (static_cast<size_t>(g) * KB + col0 / 128) * p.ld + m;
 #pragma unroll
-      for (int j = 0; j < kCastSpans; ++j) {
-        const int col = (c * kCastSpans + j) * 256 + lane * 8;
-        if (col >= p.K) continue;
-        *reinterpret_cast<uint2*>(p.A + static_cast<size_t>(row) * p.K + col) = code[j];
-        if ((lane & 15) == 0) p.sfa[(static_cast<size_t>(g) * KB + col / 128) * p.ld + m] = scale[j];
+      for (int j = 0; j < kDispatchSpans; ++j) {
+        if (col0 + j * 512 >= p.K) continue;
+        *reinterpret_cast<uint4*>(dst + j * 512) = code[j];
+        if ((lane & 7) == 0) sdst[static_cast<size_t>(4 * j) * p.ld] = scale[j];
       }
     }
   }
@@ -237,31 +298,52 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&f)[8]) {
   return *reinterpret_cast<const uint4*>(h);
 }
 
-// out[t] = sum_j weights[t][j] C[rows[t][j]] in fp32, rounded once.  One warp per token and 256
-// columns, 8 per lane.
+// out[t] = sum_j weights[t][j] C[rows[t][j]] in fp32, rounded once.  One warp per token and 256 columns,
+// 8 per lane.  B rows are asked for before the first is used: with two choices B = 2 and all the
+// warps that an SM holds keep enough bytes on the way, with more B = 4.
+template <int B>
 __global__ void __launch_bounds__(256) moe_combine_kernel(const CombineParams p, int chunks) {
   const int lane = threadIdx.x & 31;
-  const long long nwarps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
+  const long long first = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const int nwarps = static_cast<int>((gridDim.x * blockDim.x) >> 5);
+  const int step_t = nwarps / chunks, step_c = nwarps % chunks;
+  long long t = first / chunks;
+  int c = static_cast<int>(first % chunks);
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  for (long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; w < p.T * chunks;
-       w += nwarps) {
-    const long long t = w / chunks;
-    const int col = static_cast<int>(w - t * chunks) * 256 + lane * 8;
+  for (; t < p.T; t += step_t, c += step_c) {
+    if (c >= chunks) {
+      c -= chunks;
+      if (++t >= p.T) break;
+    }
+    const int col = c * 256 + lane * 8;
+    const bool in = col < p.N;
     int mine = lane < p.k ? p.rows[t * p.k + lane] : -1;
     if (mine >= p.M) mine = -1;
     const float mw = mine >= 0 ? (p.weights ? p.weights[t * p.k + lane] : 1.0f) : 0.0f;
     float acc[8] = {};
-    for (int q = 0; q < p.k; ++q) {
-      const int row = __shfl_sync(0xffffffffu, mine, q);
-      const float wq = __shfl_sync(0xffffffffu, mw, q);
-      if (row < 0 || col >= p.N) continue;
-      float f[8];
-      unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(p.C + static_cast<size_t>(row) * p.N + col)), f);
+    for (int q0 = 0; q0 < p.k; q0 += B) {
+      uint4 raw[B];
+      float wq[B];
+      bool has[B];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = fmaf(wq, f[i], acc[i]);
+      for (int q = 0; q < B; ++q) {
+        const int row = __shfl_sync(0xffffffffu, mine, (q0 + q) & 31);
+        wq[q] = __shfl_sync(0xffffffffu, mw, (q0 + q) & 31);
+        has[q] = q0 + q < p.k && row >= 0;
+        raw[q] = has[q] && in ? __ldg(reinterpret_cast<const uint4*>(p.C + static_cast<size_t>(row) * p.N + col))
+                              : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int q = 0; q < B; ++q) {
+        if (!has[q]) continue;
+        float f[8];
+        unpack_bf16x8(raw[q], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(wq[q], f[i], acc[i]);
+      }
     }
-    if (col < p.N) *reinterpret_cast<uint4*>(p.out + t * p.N + col) = pack_bf16x8(acc);
+    if (in) *reinterpret_cast<uint4*>(p.out + t * p.N + col) = pack_bf16x8(acc);
   }
 }
 
@@ -276,55 +358,94 @@ struct CombineGradParams {
   int k, N, M;
 };
 
+// Sums of eight values over a warp; lane 4 j gets the j-th.  Each step halves the values, not only the lanes.
+__device__ __forceinline__ float warp_sum8(float (&v)[8], int lane) {
+  float a[4], b[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool up = lane & 16;
+    a[i] = (up ? v[i + 4] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 4], 16);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const bool up = lane & 8;
+    b[i] = (up ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, up ? a[i] : a[i + 2], 8);
+  }
+  const bool up = lane & 4;
+  float c = (up ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, up ? b[0] : b[1], 4);
+  c += __shfl_xor_sync(0xffffffffu, c, 2);
+  return c + __shfl_xor_sync(0xffffffffu, c, 1);
+}
+
 // grad_C[rows[t][j]] = weights[t][j] grad_out[t];  grad_weights[t][j] = <grad_out[t], C[rows[t][j]]>.
-// One CTA per token; eight choices at a time, their dot products in registers.
-__global__ void __launch_bounds__(256) moe_combine_backward_kernel(const CombineGradParams p) {
-  __shared__ float s_dot[8][8];
+// One CTA per token, 16 columns per thread and pass; eight choices at a time, their dot products in
+// registers, the rows of four asked for before the first is used.
+constexpr int kCombineGradThreads = 128;
+__global__ void __launch_bounds__(kCombineGradThreads) moe_combine_backward_kernel(const CombineGradParams p) {
+  constexpr int W = kCombineGradThreads / 32, SPAN = kCombineGradThreads * 8;
+  __shared__ float s_dot[2][W][8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int buf = 0;
   pdl_wait_prior_grid();
   pdl_launch_dependents();
   for (long long t = blockIdx.x; t < p.T; t += gridDim.x) {
     for (int j0 = 0; j0 < p.k; j0 += 8) {
-      int row[8];
-      float w[8], dot[8];
+      const int j_here = j0 + (lane & 7);
+      int mine = j_here < p.k ? p.rows[t * p.k + j_here] : -1;
+      if (mine >= p.M) mine = -1;
+      const float mw = mine >= 0 ? p.weights[t * p.k + j_here] : 0.0f;
+      float dot[8] = {};
+      for (int col = threadIdx.x * 8; col - static_cast<int>(threadIdx.x) * 8 < p.N; col += 2 * SPAN) {
+        const bool first = col < p.N, second = col + SPAN < p.N;
+        const uint4* gsrc = reinterpret_cast<const uint4*>(p.grad_out + t * p.N + col);
+        uint4 graw[2];
+        graw[0] = first ? __ldg(gsrc) : make_uint4(0u, 0u, 0u, 0u);
+        graw[1] = second ? __ldg(gsrc + SPAN / 8) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        row[j] = j0 + j < p.k ? p.rows[t * p.k + j0 + j] : -1;
-        if (row[j] >= p.M) row[j] = -1;
-        w[j] = row[j] >= 0 ? p.weights[t * p.k + j0 + j] : 0.0f;
-        dot[j] = 0.0f;
-      }
-      for (int col = threadIdx.x * 8; col < p.N; col += 256 * 8) {
-        float g[8];
-        unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(p.grad_out + t * p.N + col)), g);
+        for (int jb = 0; jb < 8; jb += 4) {
+          if (j0 + jb >= p.k) break;
+          uint4 raw[4][2];
+          int row[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (row[j] < 0) continue;
-          const size_t at = static_cast<size_t>(row[j]) * p.N + col;
-          float f[8], o[8];
-          unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(p.C + at)), f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            dot[j] = fmaf(g[i], f[i], dot[j]);
-            o[i] = w[j] * g[i];
+          for (int j = 0; j < 4; ++j) {
+            row[j] = __shfl_sync(0xffffffffu, mine, jb + j);
+            const uint4* src = reinterpret_cast<const uint4*>(p.C + static_cast<size_t>(max(row[j], 0)) * p.N + col);
+            raw[j][0] = row[j] >= 0 && first ? __ldg(src) : make_uint4(0u, 0u, 0u, 0u);
+            raw[j][1] = row[j] >= 0 && second ? __ldg(src + SPAN / 8) : make_uint4(0u, 0u, 0u, 0u);
           }
-          *reinterpret_cast<uint4*>(p.grad_C + at) = pack_bf16x8(o);
+          float g[2][8];
+          unpack_bf16x8(graw[0], g[0]);
+          unpack_bf16x8(graw[1], g[1]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float w = __shfl_sync(0xffffffffu, mw, jb + j);
+            if (row[j] < 0) continue;
+            uint4* dst = reinterpret_cast<uint4*>(p.grad_C + static_cast<size_t>(row[j]) * p.N + col);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float f[8], o[8];
+              unpack_bf16x8(raw[j][h], f);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                dot[jb + j] = fmaf(g[h][i], f[i], dot[jb + j]);
+                o[i] = w * g[h][i];
+              }
+              if (h == 0 ? first : second) dst[h * (SPAN / 8)] = pack_bf16x8(o);
+            }
+          }
         }
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
-        if (lane == 0) s_dot[warp][j] = dot[j];
-      }
+      __syncwarp();
+      const float v = warp_sum8(dot, lane);
+      if ((lane & 3) == 0) s_dot[buf][warp][lane >> 2] = v;
       __syncthreads();
       if (threadIdx.x < 8 && j0 + static_cast<int>(threadIdx.x) < p.k) {
-        float v = 0.0f;
+        float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v += s_dot[i][threadIdx.x];
-        p.grad_weights[t * p.k + j0 + threadIdx.x] = v;
+        for (int i = 0; i < W; ++i) sum += s_dot[buf][i][threadIdx.x];
+        p.grad_weights[t * p.k + j0 + threadIdx.x] = sum;
       }
-      __syncthreads();
+      buf ^= 1;  // the other buffer's readers are past the barrier above
     }
   }
 }

@@ -65,6 +65,32 @@ fg_status launch(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
   return FG_OK;
 }
 
+// CTAs of a kernel that the device holds at once: the grid of a kernel whose CTAs walk over their work
+// (more would run as a second, mostly empty wave).  0 if the device cannot be asked.
+template <auto KERNEL>
+long long resident_ctas(int threads) {
+  static std::atomic<int> cached[kMaxDevices];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  int n = cached[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, KERNEL, threads, 0) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      return 0;
+    }
+    cached[dev].store(n, std::memory_order_relaxed);
+  }
+  return static_cast<long long>(n) * sm_count();
+}
+
+// Launch with one CTA per `work` unit, as many as the device holds at once.
+template <auto KERNEL, typename... Args>
+fg_status launch_walk(long long work, int threads, void* stream, const Args&... args) {
+  const long long most = resident_ctas<KERNEL>(threads);
+  if (most <= 0) return FG_ERR_CUDA;
+  return launch(KERNEL, dim3(static_cast<unsigned>(work < most ? work : most)), threads, 0, stream, 1, args...);
+}
+
 // The opt-in shared-memory size of a kernel, set once per device (not again during a capture).
 template <auto KERNEL>
 bool allow_smem(size_t bytes) {
@@ -164,28 +190,51 @@ size_t route_scratch_bytes(int S, int E, const RouteSplit& r) {
 }
 
 // ------------------------------------------------------------------------------------ row layouts
-int layout_chunks(long long pairs) { return static_cast<int>(cdiv(pairs, fg::kLayoutChunk)); }
+// Pairs per thread: 2 while that leaves a CTA per SM or fewer, else 8; one CTA (and one launch) up to 2048.
+int layout_items(long long pairs) {
+  const long long two = 2 * fg::kLayoutThreads;
+  return pairs <= two || (pairs > 4 * two && pairs <= 148 * two) ? 2 : 8;
+}
+int layout_chunks(long long pairs) {
+  return static_cast<int>(cdiv(pairs, static_cast<long long>(layout_items(pairs)) * fg::kLayoutThreads));
+}
 
-fg_status layout_run(const int* ids, int* rows, int* group, long long pairs, int E, int M, int mmax, void* scratch,
-                     size_t scratch_bytes, void* stream) {
+template <int ITEMS>
+fg_status layout_launch(const fg::LayoutParams& p, void* stream) {
+  if (p.chunks > 1) {
+    const fg_status s = launch(fg::moe_layout_count_kernel<ITEMS>, dim3(p.chunks), fg::kLayoutThreads, 0, stream, 1, p);
+    if (s != FG_OK) return s;
+  }
+  return launch(fg::moe_layout_kernel<ITEMS>, dim3(p.chunks > 0 ? p.chunks : 1), fg::kLayoutThreads, 0, stream, 1, p);
+}
+
+size_t layout_hist_bytes(long long pairs, int E) {
+  const int chunks = layout_chunks(pairs);
+  return chunks > 1 ? static_cast<size_t>(chunks) * E * 4 : 0;
+}
+
+fg_status layout_run(fg::LayoutParams& p, void* stream) {
+  p.chunks = layout_chunks(p.pairs);
+  return layout_items(p.pairs) == 2 ? layout_launch<2>(p, stream) : layout_launch<8>(p, stream);
+}
+
+fg_status layout_call(const int* ids, int* rows, int* group, long long pairs, int E, int M, int mmax, void* scratch,
+                      size_t scratch_bytes, void* stream) {
+  const size_t need = layout_hist_bytes(pairs, E);
+  if (need > 0 && (!scratch || scratch_bytes < need)) return FG_ERR_INVALID_ARG;
+  if (!aligned(scratch, 4)) return FG_ERR_ALIGNMENT;
   fg::LayoutParams p;
+  std::memset(&p, 0, sizeof(p));
   p.ids = ids;
   p.rows = rows;
   p.group = group;
   p.hist = static_cast<int*>(scratch);
   p.pairs = pairs;
   p.E = E;
-  p.chunks = layout_chunks(pairs);
   p.M = M;
   p.mmax = mmax;
   p.align = fg_m_alignment();
-  if (p.chunks > 1) {
-    if (!scratch || scratch_bytes < fg_moe_layout_scratch_bytes(pairs, E)) return FG_ERR_INVALID_ARG;
-    if (!aligned(scratch, 4)) return FG_ERR_ALIGNMENT;
-    const fg_status s = launch(fg::moe_layout_count_kernel, dim3(p.chunks), fg::kLayoutThreads, 0, stream, 1, p);
-    if (s != FG_OK) return s;
-  }
-  return launch(fg::moe_layout_kernel, dim3(p.chunks > 0 ? p.chunks : 1), fg::kLayoutThreads, 0, stream, 1, p);
+  return layout_run(p, stream);
 }
 
 fg_status layout_check(const int* ids, const int* rows, const int* group, long long pairs, int E) {
@@ -201,6 +250,48 @@ fg_status lora_launch(const fg::LoraParams& p, void* stream) {
   if (!allow_smem<fg::lora_rows_kernel<NT>>(smem)) return FG_ERR_CUDA;
   return launch(fg::lora_rows_kernel<NT>, dim3(static_cast<unsigned>(p.M) * fg::kLoraCluster), fg::kLoraThreads, smem,
                 stream, fg::kLoraCluster, p);
+}
+
+template <int RP>
+fg_status lora_tiles_launch(const fg::LoraParams& p, int tiles, void* stream) {
+  constexpr size_t smem = fg::LoraTile<RP>::SMEM;
+  if (!allow_smem<fg::lora_tiles_kernel<RP>>(smem)) return FG_ERR_CUDA;
+  return launch(fg::lora_tiles_kernel<RP>, dim3(static_cast<unsigned>(tiles) * fg::kLoraTileCluster), fg::kLoraThreads,
+                smem, stream, fg::kLoraTileCluster, p);
+}
+
+// Many rows per adapter: tiles of 128 rows.  Few: groups of 16, found by the kernel itself.
+bool lora_by_tiles(int M, int L) { return L > 0 && L < FG_MOE_MAX_EXPERTS && M <= (1 << 24) && M > 256; }
+
+// Places of the sorted rows: tiles of the L adapters and of the rows without one.
+int lora_places(int M, int L) {
+  const int n = M < L + 1 ? M : L + 1;
+  return fg::kLoraTileRows * (n + (M - n) / fg::kLoraTileRows);
+}
+size_t lora_scratch_bytes(int M, int L) {
+  if (!lora_by_tiles(M, L)) return 0;
+  return static_cast<size_t>(lora_places(M, L)) * 8 + layout_hist_bytes(M, L + 1);
+}
+
+__device__ int g_lora_status;  // FG_ERR_TIMEOUT once a wait of lora_tiles_kernel has run out
+
+// Its address, looked up once per device (not again during a capture).
+int* lora_status_word() {
+  static std::atomic<int*> cached[kMaxDevices];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  int* at = cached[dev].load(std::memory_order_acquire);
+  if (at) return at;
+  void* v = nullptr;
+  if (cudaGetSymbolAddress(&v, g_lora_status) != cudaSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  cached[dev].store(static_cast<int*>(v), std::memory_order_release);
+  return static_cast<int*>(v);
 }
 
 }  // namespace
@@ -290,8 +381,8 @@ long long fg_moe_layout_rows(long long pairs, int E) {
 }
 
 size_t fg_moe_layout_scratch_bytes(long long pairs, int E) {
-  if (pairs <= fg::kLayoutChunk || E <= 0 || pairs > (1ll << 24)) return 0;
-  return static_cast<size_t>(layout_chunks(pairs)) * E * 4;
+  if (pairs <= 0 || E <= 0 || pairs > (1ll << 24)) return 0;
+  return layout_hist_bytes(pairs, E);
 }
 
 fg_status fg_moe_layout_contiguous(const int* ids, int* rows, int* m_indices, long long pairs, int E, int M,
@@ -300,7 +391,7 @@ fg_status fg_moe_layout_contiguous(const int* ids, int* rows, int* m_indices, lo
   const fg_status s = layout_check(ids, rows, m_indices, pairs, E);
   if (s != FG_OK) return s;
   if (M < fg_moe_layout_rows(pairs, E)) return FG_ERR_INVALID_ARG;
-  return layout_run(ids, rows, m_indices, pairs, E, M, 0, scratch, scratch_bytes, stream);
+  return layout_call(ids, rows, m_indices, pairs, E, M, 0, scratch, scratch_bytes, stream);
 }
 
 fg_status fg_moe_layout_masked(const int* ids, int* rows, int* masked_m, long long pairs, int E, int mmax,
@@ -309,7 +400,7 @@ fg_status fg_moe_layout_masked(const int* ids, int* rows, int* masked_m, long lo
   if (s != FG_OK) return s;
   if (mmax <= 0) return FG_ERR_INVALID_ARG;
   if (static_cast<long long>(E) * mmax > 0x7fffffffll) return FG_ERR_UNSUPPORTED;
-  return layout_run(ids, rows, masked_m, pairs, E, 0, mmax, scratch, scratch_bytes, stream);
+  return layout_call(ids, rows, masked_m, pairs, E, 0, mmax, scratch, scratch_bytes, stream);
 }
 
 fg_status fg_moe_dispatch_fp8(const void* x, const int* rows, void* A, float* sfa, int T, int k, int G, int M, int K,
@@ -320,8 +411,6 @@ fg_status fg_moe_dispatch_fp8(const void* x, const int* rows, void* A, float* sf
   if (K % 16 != 0 || !aligned(x, 16) || !aligned(A, 16) || !aligned(sfa, 4) || !aligned(rows, 4))
     return FG_ERR_ALIGNMENT;
   if (k > fg::kRowsMaxK || static_cast<long long>(G) * M > 0x7fffffffll) return FG_ERR_UNSUPPORTED;
-  const int sms = sm_count();
-  if (sms <= 0) return FG_ERR_CUDA;
   fg::DispatchParams p;
   p.x = static_cast<const __nv_bfloat16*>(x);
   p.rows = rows;
@@ -333,11 +422,10 @@ fg_status fg_moe_dispatch_fp8(const void* x, const int* rows, void* A, float* sf
   p.M = G * M;
   p.mmax = M;
   p.ld = fg_sfa_ld(M);
-  const int chunks = static_cast<int>(cdiv(K, 256 * fg::kCastSpans));
-  long long blocks = cdiv(static_cast<long long>(T) * chunks, 8);
-  if (blocks > 8ll * sms) blocks = 8ll * sms;
-  const auto kernel = fmt == FG_E4M3 ? fg::moe_dispatch_kernel<0> : fg::moe_dispatch_kernel<1>;
-  return launch(kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, 1, p, chunks);
+  const int chunks = static_cast<int>(cdiv(K, 512 * fg::kDispatchSpans));
+  const long long blocks = cdiv(static_cast<long long>(T) * chunks, 8);
+  return fmt == FG_E4M3 ? launch_walk<fg::moe_dispatch_kernel<0>>(blocks, 256, stream, p, chunks)
+                        : launch_walk<fg::moe_dispatch_kernel<1>>(blocks, 256, stream, p, chunks);
 }
 
 static fg_status combine_check(int T, int k, int M, int N) {
@@ -354,8 +442,6 @@ fg_status fg_moe_combine(const void* C, const int* rows, const float* weights, v
   if (T == 0 || N == 0) return FG_OK;
   if (!out || (k > 0 && (!rows || (M > 0 && !C)))) return FG_ERR_INVALID_ARG;
   if (!aligned(C, 16) || !aligned(out, 16) || !aligned(rows, 4) || !aligned(weights, 4)) return FG_ERR_ALIGNMENT;
-  const int sms = sm_count();
-  if (sms <= 0) return FG_ERR_CUDA;
   fg::CombineParams p;
   p.C = static_cast<const __nv_bfloat16*>(C);
   p.rows = rows;
@@ -366,9 +452,9 @@ fg_status fg_moe_combine(const void* C, const int* rows, const float* weights, v
   p.N = N;
   p.M = M;
   const int chunks = static_cast<int>(cdiv(N, 256));
-  long long blocks = cdiv(static_cast<long long>(T) * chunks, 8);
-  if (blocks > 8ll * sms) blocks = 8ll * sms;
-  return launch(fg::moe_combine_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, 1, p, chunks);
+  const long long blocks = cdiv(static_cast<long long>(T) * chunks, 8);
+  return k <= 2 ? launch_walk<fg::moe_combine_kernel<2>>(blocks, 256, stream, p, chunks)
+                : launch_walk<fg::moe_combine_kernel<4>>(blocks, 256, stream, p, chunks);
 }
 
 fg_status fg_moe_combine_backward(const void* grad_out, const void* C, const int* rows, const float* weights,
@@ -381,8 +467,6 @@ fg_status fg_moe_combine_backward(const void* grad_out, const void* C, const int
   if (!aligned(grad_out, 16) || !aligned(C, 16) || !aligned(grad_C, 16) || !aligned(rows, 4) || !aligned(weights, 4) ||
       !aligned(grad_weights, 4))
     return FG_ERR_ALIGNMENT;
-  const int sms = sm_count();
-  if (sms <= 0) return FG_ERR_CUDA;
   fg::CombineGradParams p;
   p.grad_out = static_cast<const __nv_bfloat16*>(grad_out);
   p.C = static_cast<const __nv_bfloat16*>(C);
@@ -394,12 +478,14 @@ fg_status fg_moe_combine_backward(const void* grad_out, const void* C, const int
   p.k = k;
   p.N = N;
   p.M = M;
-  const int blocks = T < 8 * sms ? T : 8 * sms;
-  return launch(fg::moe_combine_backward_kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, 1, p);
+  return launch_walk<fg::moe_combine_backward_kernel>(T, fg::kCombineGradThreads, stream, p);
 }
 
+size_t fg_lora_scratch_bytes(int M, int L) { return M > 0 && L > 0 ? lora_scratch_bytes(M, L) : 0; }
+
 fg_status fg_lora_add(const void* C, const void* x, const void* lora_a, const void* lora_b, const int* adapters,
-                      const float* scaling, void* out, int M, int N, int K, int R, int L, void* stream) {
+                      const float* scaling, void* out, int M, int N, int K, int R, int L, void* scratch,
+                      size_t scratch_bytes, void* stream) {
   if (M < 0 || N < 0 || K < 0 || R < 0 || L < 0) return FG_ERR_INVALID_ARG;
   if (K % 16 != 0 || N % 8 != 0 || R % 8 != 0) return FG_ERR_ALIGNMENT;
   if (R > fg::kLoraMaxRank) return FG_ERR_UNSUPPORTED;
@@ -408,9 +494,10 @@ fg_status fg_lora_add(const void* C, const void* x, const void* lora_a, const vo
   if (K == 0 || R == 0) L = 0;  // no adapter adds anything
   if (L > 0 && (!x || !lora_a || !lora_b)) return FG_ERR_INVALID_ARG;
   if (!aligned(C, 16) || !aligned(x, 16) || !aligned(lora_a, 16) || !aligned(lora_b, 16) || !aligned(out, 16) ||
-      !aligned(adapters, 4) || !aligned(scaling, 4))
+      !aligned(adapters, 4) || !aligned(scaling, 4) || !aligned(scratch, 4))
     return FG_ERR_ALIGNMENT;
   fg::LoraParams p;
+  std::memset(&p, 0, sizeof(p));
   p.C = static_cast<const __nv_bfloat16*>(C);
   p.x = static_cast<const __nv_bfloat16*>(x);
   p.a = static_cast<const __nv_bfloat16*>(lora_a);
@@ -423,11 +510,49 @@ fg_status fg_lora_add(const void* C, const void* x, const void* lora_a, const vo
   p.K = K;
   p.R = R;
   p.L = L;
+  if (lora_by_tiles(M, L)) {
+    if (!scratch || scratch_bytes < lora_scratch_bytes(M, L)) return FG_ERR_INVALID_ARG;
+    p.status = lora_status_word();
+    if (!p.status) return FG_ERR_CUDA;
+    fg::LayoutParams lp;
+    std::memset(&lp, 0, sizeof(lp));
+    lp.M = lora_places(M, L);
+    lp.ids = adapters;
+    lp.group = static_cast<int*>(scratch);
+    lp.inverse = lp.group + lp.M;
+    lp.hist = lp.inverse + lp.M;
+    lp.pairs = M;
+    lp.E = L + 1;
+    lp.align = fg::kLoraTileRows;
+    lp.rest = 1;
+    p.group = lp.group;
+    p.place_row = lp.inverse;
+    const fg_status s = layout_run(lp, stream);
+    if (s != FG_OK) return s;
+    const int tiles = lp.M / fg::kLoraTileRows;
+    if (R <= 16) return lora_tiles_launch<16>(p, tiles, stream);
+    if (R <= 32) return lora_tiles_launch<32>(p, tiles, stream);
+    if (R <= 64) return lora_tiles_launch<64>(p, tiles, stream);
+    return lora_tiles_launch<128>(p, tiles, stream);
+  }
   if (R <= 8) return lora_launch<1>(p, stream);
   if (R <= 16) return lora_launch<2>(p, stream);
   if (R <= 32) return lora_launch<4>(p, stream);
   if (R <= 64) return lora_launch<8>(p, stream);
   return lora_launch<16>(p, stream);
+}
+
+fg_status fg_lora_status(void* stream) {
+  int* at = lora_status_word();
+  if (!at) return FG_ERR_CUDA;
+  int v = 0;
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess ||
+      cudaMemcpy(&v, at, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess ||
+      (v != 0 && cudaMemset(at, 0, sizeof(int)) != cudaSuccess)) {
+    cudaGetLastError();
+    return FG_ERR_CUDA;
+  }
+  return static_cast<fg_status>(v);
 }
 
 }  // extern "C"

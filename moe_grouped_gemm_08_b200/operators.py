@@ -323,6 +323,15 @@ def lora_add(C, x, lora_a, lora_b, adapters, scaling=None, out=None, stream=None
         return _there(dev, stream, lora_add, C, x, lora_a, lora_b, adapters, scaling, out)
     if out is None:
         out = torch.empty_like(C)
+    size = _lib.fg_lora_scratch_bytes(M, L)
+    scratch, at = _scratch(size, dev)
     _check(_lib.fg_lora_add(C.data_ptr(), x.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(), adapters.data_ptr(),
-                            _ptr(scaling), out.data_ptr(), M, N, K, R, L, _raw_stream(dev.index)), "fg_lora_add")
+                            _ptr(scaling), out.data_ptr(), M, N, K, R, L, at, size, _raw_stream(dev.index)),
+           "fg_lora_add")
     return out
+
+
+def lora_status(stream=None) -> int:
+    """Synchronise the stream, then read and clear the status of lora_add on the current device: 0, or
+    6 (FG_ERR_TIMEOUT) if a wait of one of its kernels has run out since the last read."""
+    return int(_lib.fg_lora_status(_stream(stream)))

@@ -106,7 +106,8 @@ def test_combine_argument_errors():
     (dict(x=P + 8), 2), (dict(out=P + 8), 2), (dict(scaling=P + 2), 2), (dict(M=0), 0), (dict(N=0), 0),
 ])
 def test_lora_argument_errors(change, expect):
-    a = dict(C=P, x=P, a=P, b=P, ids=P, scaling=NULL, out=P, M=4, N=64, K=64, R=16, L=2, stream=NULL)
+    a = dict(C=P, x=P, a=P, b=P, ids=P, scaling=NULL, out=P, M=4, N=64, K=64, R=16, L=2, scratch=NULL, bytes=0,
+             stream=NULL)
     a.update(change)
     assert fg.lib.fg_lora_add(*a.values()) == expect
 
