@@ -299,48 +299,55 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&f)[8]) {
 }
 
 // out[t] = sum_j weights[t][j] C[rows[t][j]] in fp32, rounded once.  One warp per token and 256 columns,
-// 8 per lane.  B rows are asked for before the first is used: with two choices B = 2 and all the
-// warps that an SM holds keep enough bytes on the way, with more B = 4.
+// 8 per lane.  B = 4: four rows are asked for before the first is used (8 choices of 2048 columns: 27
+// us for 151 MB, 32 us with B = 1); with one or two choices B = 1, whose 32 registers let an SM hold 64 warps
+// (2 choices of 7168 columns: 121 us for 705 MB, 137 us with B = 2).
 template <int B>
-__global__ void __launch_bounds__(256) moe_combine_kernel(const CombineParams p, int chunks) {
+__global__ void __launch_bounds__(256, B == 1 ? 8 : 5) moe_combine_kernel(const CombineParams p, int chunks) {
   const int lane = threadIdx.x & 31;
-  const long long first = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int nwarps = static_cast<int>((gridDim.x * blockDim.x) >> 5);
-  const int step_t = nwarps / chunks, step_c = nwarps % chunks;
-  long long t = first / chunks;
-  int c = static_cast<int>(first % chunks);
+  const long long nwarps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  for (; t < p.T; t += step_t, c += step_c) {
-    if (c >= chunks) {
-      c -= chunks;
-      if (++t >= p.T) break;
-    }
-    const int col = c * 256 + lane * 8;
+  for (long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; w < p.T * chunks;
+       w += nwarps) {
+    const long long t = w / chunks;
+    const int col = static_cast<int>(w - t * chunks) * 256 + lane * 8;
     const bool in = col < p.N;
     int mine = lane < p.k ? p.rows[t * p.k + lane] : -1;
     if (mine >= p.M) mine = -1;
     const float mw = mine >= 0 ? (p.weights ? p.weights[t * p.k + lane] : 1.0f) : 0.0f;
     float acc[8] = {};
-    for (int q0 = 0; q0 < p.k; q0 += B) {
-      uint4 raw[B];
-      float wq[B];
-      bool has[B];
-#pragma unroll
-      for (int q = 0; q < B; ++q) {
-        const int row = __shfl_sync(0xffffffffu, mine, (q0 + q) & 31);
-        wq[q] = __shfl_sync(0xffffffffu, mw, (q0 + q) & 31);
-        has[q] = q0 + q < p.k && row >= 0;
-        raw[q] = has[q] && in ? __ldg(reinterpret_cast<const uint4*>(p.C + static_cast<size_t>(row) * p.N + col))
-                              : make_uint4(0u, 0u, 0u, 0u);
-      }
-#pragma unroll
-      for (int q = 0; q < B; ++q) {
-        if (!has[q]) continue;
+    if constexpr (B == 1) {
+      for (int q = 0; q < p.k; ++q) {
+        const int row = __shfl_sync(0xffffffffu, mine, q);
+        const float wq = __shfl_sync(0xffffffffu, mw, q);
+        if (row < 0 || !in) continue;
         float f[8];
-        unpack_bf16x8(raw[q], f);
+        unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(p.C + static_cast<size_t>(row) * p.N + col)), f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = fmaf(wq[q], f[i], acc[i]);
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(wq, f[i], acc[i]);
+      }
+    } else {
+      for (int q0 = 0; q0 < p.k; q0 += B) {
+        uint4 raw[B];
+        float wq[B];
+        bool has[B];
+#pragma unroll
+        for (int q = 0; q < B; ++q) {
+          const int row = __shfl_sync(0xffffffffu, mine, (q0 + q) & 31);
+          wq[q] = __shfl_sync(0xffffffffu, mw, (q0 + q) & 31);
+          has[q] = q0 + q < p.k && row >= 0;
+          raw[q] = has[q] && in ? __ldg(reinterpret_cast<const uint4*>(p.C + static_cast<size_t>(row) * p.N + col))
+                                : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int q = 0; q < B; ++q) {
+          if (!has[q]) continue;
+          float f[8];
+          unpack_bf16x8(raw[q], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i] = fmaf(wq[q], f[i], acc[i]);
+        }
       }
     }
     if (in) *reinterpret_cast<uint4*>(p.out + t * p.N + col) = pack_bf16x8(acc);
