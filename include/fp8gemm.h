@@ -311,10 +311,10 @@ fg_status fg_moe_combine_backward(const void* grad_out, const void* C, const int
  * Both products accumulate in fp32, A_a x is kept to 16 bits of mantissa between them, and the sum
  * is rounded once.  K % 16 == 0, N % 8 == 0, R % 8 == 0, R <= 128 (a smaller rank is padded with
  * zeros).  Rows of one adapter may stand anywhere; many rows are first sorted by adapter, which
- * takes the scratch.  The first call on a device is made outside stream capture.
- * A wait of the kernel for many rows that runs out (about two seconds) makes it write NaN and leave
+ * takes the scratch (16-byte aligned).  The first call on a device is made outside stream capture.
+ * A wait of a kernel for many rows that runs out (about two seconds) makes it write NaN and leave
  * FG_ERR_TIMEOUT for fg_lora_status, which synchronises `stream`, reads and clears it. */
-size_t fg_lora_scratch_bytes(int M, int L);
+size_t fg_lora_scratch_bytes(int M, int R, int L);
 fg_status fg_lora_add(const void* C, const void* x, const void* lora_a, const void* lora_b,
                       const int* adapters, const float* scaling, void* out, int M, int N, int K, int R, int L,
                       void* scratch, size_t scratch_bytes, void* stream);

@@ -127,7 +127,7 @@ def _declare(l: ctypes.CDLL) -> ctypes.CDLL:
     l.fg_moe_combine.restype = _int
     l.fg_moe_combine_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _int, _int, _int, _int, _vp]
     l.fg_moe_combine_backward.restype = _int
-    l.fg_lora_scratch_bytes.argtypes = [_int, _int]
+    l.fg_lora_scratch_bytes.argtypes = [_int, _int, _int]
     l.fg_lora_scratch_bytes.restype = ctypes.c_size_t
     l.fg_lora_add.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _int, _int, _int, _int, _int, _vp, ctypes.c_size_t,
                               _vp]

@@ -25,9 +25,13 @@ struct LoraParams {
   const float* scaling;  // [L] or nullptr (all 1)
   __nv_bfloat16* out;
   int M, N, K, R, L;
-  // tiles of rows sorted by adapter (lora_tiles_kernel): place -> adapter (L: none, -1: padding) and row
-  const int* group;
-  const int* place_row;
+  // many rows: places of the rows sorted by adapter, in tiles of 128
+  const int* group;      // place -> adapter (L: none, -1: padding)
+  const int* place_row;  // place -> row
+  const int* tiles;      // tiles of adapters, tiles in all
+  int* counters;         // per tile: parts of h written so far (zero before)
+  float* parts;          // [2 * CTAs][rank padded / 4][128][4]: parts of h
+  uint8_t* h;            // per tile: h in two bf16 halves, as tcgen05.mma reads them
   int* status;
 };
 
@@ -234,46 +238,46 @@ __global__ void __launch_bounds__(kLoraThreads) lora_rows_kernel(const LoraParam
 }
 
 // ---------------------------------------------------------------------------- many rows
-// Tiles of 128 rows of one adapter, one cluster of four CTAs each, both products on the tensor cores:
-//   1. a rank forms its part of h = x A^T over a quarter of K: 64 columns a stage, the rows of x gathered and the
-//      rows of A copied by cp.async into 128-byte-swizzled tiles, tcgen05.mma into TMEM;
-//   2. the four parts are summed in rank order, each rank summing 32 rows over distributed shared memory
-//      and handing them, scaled and split into two bf16 halves, to all four;
-//   3. each rank adds h B^T to its quarter of the columns of C, 64 at a time: C and B by cp.async, the
-//      product into one of two TMEM buffers, while the chunk before is added and stored.
-// Bound by HBM (x, C in and out); two CTAs share an SM (ranks up to 64), so that one's phases overlap
-// the other's and a few tiles more than SMs do not cost a second wave.  mma.sync for the second product
-// measured 28 us of a 45 us tile where this takes the time of its bytes.
+// Rows sorted by adapter, tiles of 128 of one adapter, both products on the tensor cores, in two kernels of
+// one CTA per SM:
+//   lora_down_kernel  h = scaling x A^T.  The (tile, 64 columns of K) units are split evenly over the CTAs, so that a
+//                     few tiles more or less than SMs cost nothing; x gathered and A copied by cp.async into
+//                     128-byte-swizzled tiles, up to ten stages deep, tcgen05.mma into TMEM.  A tile that
+//                     several CTAs share is summed by the last of them, in the CTAs' order, and kept as two bf16
+//                     halves (hi + lo: 16 bits of h).
+//   lora_up_kernel    out = C + h B^T, the (tile, 64 columns of N) units split the same way: C and B by cp.async, the product
+//                     into one of two TMEM buffers while the chunk before is added and stored.
+// Bound by HBM: x once, C in and out.  (mma.sync took 28 us for the second product of 4096 x 4096, rank
+// 64, whose bytes take 11; one fused kernel, four CTAs of a cluster per tile, took 54 us in all.)
 constexpr int kLoraTileRows = 128;
-constexpr int kLoraTileCluster = 4;
-constexpr int kLoraRing = 3;                     // chunks of C and B in shared memory
 constexpr uint64_t kLoraWaitNs = 2000000000ull;  // far above any legal wait
 constexpr int kLoraTimeout = 6;                  // FG_ERR_TIMEOUT
+constexpr int kLoraLeastUnits = 8;               // K units that a CTA takes at least (bounds a tile's parts)
 
 template <int RP>
 struct LoraTile {
-  static constexpr int LD = RP + 4;                     // row of a part of h, floats
-  static constexpr int KB = (RP + 63) / 64;             // 64-wide blocks of the rank
-  static constexpr int X_BYTES = kLoraTileRows * 128;   // 128 rows x 64 columns
-  static constexpr int STAGES = RP <= 64 ? 4 : 5;
+  static constexpr int KB = (RP + 63) / 64;            // 64-wide blocks of the rank
+  static constexpr int X_BYTES = kLoraTileRows * 128;  // 128 rows x 64 columns
   static constexpr int STAGE_BYTES = X_BYTES + RP * 128;
-  static constexpr int H_BYTES = KB * X_BYTES;          // one half of h
-  static constexpr int PART = 2 * H_BYTES;              // offsets: the part of h; the rings
-  static constexpr int C_RING = 2 * H_BYTES;
-  static constexpr int B_RING = C_RING + kLoraRing * X_BYTES;
+  static constexpr int STAGES = 200 * 1024 / STAGE_BYTES;
+  static constexpr int DOWN_SMEM = 1024 + STAGES * STAGE_BYTES;
+  static constexpr int PART_FLOATS = kLoraTileRows * RP;
+  static constexpr int H_BYTES = KB * X_BYTES;  // one half of h
   static constexpr int B_BYTES = KB * 64 * 128;
-  static constexpr int END = B_RING + kLoraRing * B_BYTES;
-  static constexpr int SMEM = 1024 + (END > STAGES * STAGE_BYTES ? END : STAGES * STAGE_BYTES);
-  static_assert(PART + kLoraTileRows * LD * 4 <= SMEM - 1024, "part of h");
-  static_assert(SMEM <= 227 * 1024 && (RP > 64 || 2 * (SMEM + 2048) <= 227 * 1024), "shared memory");
+  static constexpr int RING = RP <= 64 ? 7 : 4;  // chunks of C and B in shared memory
+  static constexpr int UP_SMEM = 1024 + 2 * H_BYTES + RING * (X_BYTES + B_BYTES);
+  static_assert(DOWN_SMEM <= 225 * 1024 && UP_SMEM <= 225 * 1024, "shared memory");
 };
+
+// Units [begin(c), begin(c + 1)) of U belong to CTA c of P; U >= P.
+__device__ __forceinline__ int lora_begin(int c, int P, long long U) { return static_cast<int>(c * U / P); }
+__device__ __forceinline__ int lora_owner(int u, int P, long long U) {
+  return static_cast<int>(((static_cast<long long>(u) + 1) * P - 1) / U);
+}
 
 // 16 bytes global -> shared, zeros where `in` is false (the address must be valid all the same).
 __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void st_dsmem_2(uint32_t cluster_addr, uint32_t a, uint32_t b) {
-  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(cluster_addr), "r"(a), "r"(b) : "memory");
 }
 __device__ __forceinline__ uint4 ld_shared_16(uint32_t addr) {
   uint4 v;
@@ -283,8 +287,6 @@ __device__ __forceinline__ uint4 ld_shared_16(uint32_t addr) {
 __device__ __forceinline__ void st_shared_16(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-// Orders generic-proxy writes to shared memory of the cluster before later accesses of the async proxy.
-__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 // D[tmem] (+)= A[smem desc] * B[smem desc]^T, bf16 operands, fp32 accumulator.
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                          uint32_t accumulate) {
@@ -301,75 +303,62 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// Rows of a tile that thread `tid` copies 16 bytes of: row_of + 32 i; -1 for padding.
+__device__ __forceinline__ void lora_tile_rows(const LoraParams& p, int tile, int row_of, int (&row)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = tile * kLoraTileRows + row_of + 32 * i;
+    row[i] = p.group[at] >= 0 ? p.place_row[at] : -1;
+  }
+}
+
 template <int RP>
-__global__ void __launch_bounds__(kLoraThreads, RP <= 64 ? 2 : 1) lora_tiles_kernel(const LoraParams p) {
+__global__ void __launch_bounds__(kLoraThreads, 1) lora_down_kernel(const LoraParams p) {
   typedef LoraTile<RP> L;
   constexpr int STAGES = L::STAGES;
-  constexpr uint32_t TMEM_COLS = 128;
+  constexpr uint32_t TMEM_COLS = RP < 32 ? 32 : RP;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int s_row[kLoraTileRows];
   __shared__ __align__(8) uint64_t done[STAGES];
-  __shared__ __align__(8) uint64_t chunk_done[2];
   __shared__ uint32_t s_tmem;
+  __shared__ int s_last;
   __shared__ volatile int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = static_cast<int>(cluster_ctarank());
-  const int tile = blockIdx.x / kLoraTileCluster;
-  const uint32_t raw = smem_addr(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;  // the same in every CTA of the cluster
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   // copies: 8 threads take the 128 bytes of a row, 32 rows at once
   const int piece = tid & 7, row_of = tid >> 3;
   const uint32_t swizzled = static_cast<uint32_t>(row_of * 128 + ((piece ^ (row_of & 7)) << 4));
-
-  pdl_wait_prior_grid();
-  pdl_launch_dependents();
-  const int ad = p.group[tile * kLoraTileRows];
-  if (ad < 0 || (ad >= p.L && p.out == p.C)) return;  // the same for the whole cluster
-  if (tid < kLoraTileRows) {
-    const int at = tile * kLoraTileRows + tid;
-    s_row[tid] = p.group[at] >= 0 ? p.place_row[at] : -1;
-  }
-  const int chunks = (p.N + 63) / 64;
-  const int c0 = static_cast<int>(static_cast<long long>(chunks) * rank / kLoraTileCluster);
-  const int nc = static_cast<int>(static_cast<long long>(chunks) * (rank + 1) / kLoraTileCluster) - c0;
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) mbar_init(&done[s], 1);
-    mbar_init(&chunk_done[0], 1);
-    mbar_init(&chunk_done[1], 1);
     s_abort = 0;
     fence_mbar_init();
   }
-  if (warp == 0 && ad < p.L) {
+  pdl_wait_prior_grid();
+  pdl_launch_dependents();
+  const int KB = (p.K + 63) / 64;
+  const long long U = static_cast<long long>(p.tiles[0]) * KB;
+  const long long most = (U + kLoraLeastUnits - 1) / kLoraLeastUnits;
+  const int P = static_cast<int>(most < gridDim.x ? most : gridDim.x);
+  if (static_cast<int>(blockIdx.x) >= P) return;
+  const int u0 = lora_begin(blockIdx.x, P, U), n = lora_begin(blockIdx.x + 1, P, U) - u0;
+  if (warp == 0) {
     tmem_alloc(&s_tmem, TMEM_COLS);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  int row[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) row[i] = s_row[row_of + 32 * i];
-  if (ad >= p.L) {  // no adapter: the rows are copied
-    for (int c = c0; c < c0 + nc; ++c) {
-      const int col = c * 64 + piece * 8;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (row[i] < 0 || col >= p.N) continue;
-        const size_t at = static_cast<size_t>(row[i]) * p.N + col;
-        *reinterpret_cast<uint4*>(p.out + at) = *reinterpret_cast<const uint4*>(p.C + at);
-      }
-    }
-    return;
-  }
   const uint32_t tmem = s_tmem;
 
-  // ---- 1. this rank's part of h
-  const int kblocks = (p.K + 63) / 64;
-  const int k0 = static_cast<int>(static_cast<long long>(kblocks) * rank / kLoraTileCluster);
-  const int n = static_cast<int>(static_cast<long long>(kblocks) * (rank + 1) / kLoraTileCluster) - k0;
-  const __nv_bfloat16* wa = p.a + static_cast<size_t>(ad) * p.R * p.K;
+  int load_tile = -1, row[4];
+  const __nv_bfloat16* wa = nullptr;
   auto load = [&](int it) {
-    const int k = (k0 + it) * 64 + piece * 8;
+    const int t = (u0 + it) / KB, kb = (u0 + it) - t * KB;
+    if (t != load_tile) {
+      load_tile = t;
+      lora_tile_rows(p, t, row_of, row);
+      wa = p.a + static_cast<size_t>(p.group[t * kLoraTileRows]) * p.R * p.K;
+    }
+    const int k = kb * 64 + piece * 8;
     const bool in = k < p.K;
     const int at = in ? k : 0;
     const uint32_t st = base + (it % STAGES) * L::STAGE_BYTES + swizzled;
@@ -385,12 +374,15 @@ __global__ void __launch_bounds__(kLoraThreads, RP <= 64 ? 2 : 1) lora_tiles_ker
     }
   };
   bool ok = true;
-#pragma unroll
+#pragma unroll 1
   for (int it = 0; it < STAGES - 1; ++it) {
     if (it < n) load(it);
     cp_async_commit();
   }
+#pragma unroll 1
   for (int it = 0; it < n; ++it) {
+    const int u = u0 + it, t = u / KB, kb = u - t * KB;
+    const int from = max(t * KB, u0);  // the first unit of this tile here
     cp_async_wait<STAGES - 2>();
     fence_proxy_async_smem();
     __syncthreads();
@@ -400,174 +392,249 @@ __global__ void __launch_bounds__(kLoraThreads, RP <= 64 ? 2 : 1) lora_tiles_ker
       const uint64_t adesc = smem_desc_k128_sw128(st), bdesc = smem_desc_k128_sw128(st + L::X_BYTES);
 #pragma unroll
       for (int j = 0; j < 4; ++j)  // 16 values = 32 bytes = 2 descriptor units per step
-        mma_bf16(tmem, adesc + 2 * j, bdesc + 2 * j, idesc_bf16_f32(kLoraTileRows, RP), it + j > 0 ? 1u : 0u);
+        mma_bf16(tmem, adesc + 2 * j, bdesc + 2 * j, idesc_bf16_f32(kLoraTileRows, RP), u > from || j > 0 ? 1u : 0u);
       mma_commit(&done[it % STAGES]);
     }
     const int next = it + STAGES - 1;
     if (next < n) {
-      if (it > 0 && ok)  // the products that read this slot
+      if (it > 0 && ok)  // the products that read this place of the ring
         ok = mbar_wait(&done[next % STAGES], ((it - 1) / STAGES) & 1u, &s_abort, kLoraWaitNs);
       if (ok) load(next);
     }
     cp_async_commit();
-  }
-  if (n > 0 && ok) ok = mbar_wait(&done[(n - 1) % STAGES], ((n - 1) / STAGES) & 1u, &s_abort, kLoraWaitNs);
-  cp_async_wait<0>();
-  __syncthreads();
+    if (kb < KB - 1 && it < n - 1) continue;
 
-  // ---- 2. the parts' sum; a warp reads lane quadrant warp % 4, the columns split between the warp halves
-  tc_fence_after();
-  float* s_part = reinterpret_cast<float*>(smem_raw + (base - raw) + L::PART);
-  {
-    constexpr int CPW = RP >= 32 ? RP / 2 : RP;
-    constexpr int STEP = CPW < 32 ? 16 : 32;
-    const int first = (warp >> 2) * CPW;
-    float* dst = s_part + ((warp & 3) * 32 + lane) * L::LD;
-    if (first < RP) {
+    // the tile ends here, or this CTA's share of it does
+    if (ok) ok = mbar_wait(&done[it % STAGES], (it / STAGES) & 1u, &s_abort, kLoraWaitNs);
+    tc_fence_after();
+    const int first = lora_owner(t * KB, P, U), last = lora_owner(t * KB + KB - 1, P, U);
+    const int ad = p.group[t * kLoraTileRows];
+    const float scale = s_abort ? __int_as_float(0x7fffffff) : p.scaling ? p.scaling[ad] : 1.0f;
+    uint8_t* ht = p.h + static_cast<size_t>(t) * (2 * L::H_BYTES);
+    auto keep = [&](int m, int r, float4 v) {  // h[m][r .. r + 3] as two halves
+      uint32_t hi[2], lo[2];
+      split_bf16x2(v.x * scale, v.y * scale, hi[0], lo[0]);
+      split_bf16x2(v.z * scale, v.w * scale, hi[1], lo[1]);
+      uint8_t* at = ht + (r / 64) * L::X_BYTES + m * 128 + ((((r % 64) / 8) ^ (m & 7)) << 4) + (r & 4) * 2;
+      *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(at + L::H_BYTES) = make_uint2(lo[0], lo[1]);
+    };
+    // of the CTA's two places for parts, the first is for a tile that began in an earlier CTA
+    auto place = [&](int c) {
+      return reinterpret_cast<float4*>(p.parts + static_cast<size_t>(2 * c + (lora_begin(c, P, U) > t * KB ? 0 : 1)) *
+                                                     L::PART_FLOATS);
+    };
+    {
+      constexpr int CPW = RP >= 32 ? RP / 2 : RP;
+      constexpr int STEP = CPW < 32 ? 16 : 32;
+      const int c0 = (warp >> 2) * CPW, m = (warp & 3) * 32 + lane;
+      if (c0 < RP) {
+        float4* part = place(blockIdx.x);
 #pragma unroll
-      for (int c = 0; c < CPW; c += STEP) {
-        uint32_t v[STEP];
-        if (n > 0) {
-          const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + first + c;
+        for (int c = 0; c < CPW; c += STEP) {
+          uint32_t v[STEP];
+          const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0 + c;
           if constexpr (STEP == 16)
             tmem_ld_32x32b_x16(at, v);
           else
             tmem_ld_32x32b_x32(at, v);
           tmem_wait_ld();
-        } else {
 #pragma unroll
-          for (int i = 0; i < STEP; ++i) v[i] = 0u;
+          for (int i = 0; i < STEP; i += 4) {
+            const float4 f = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]),
+                                         __uint_as_float(v[i + 3]));
+            if (first == last)
+              keep(m, c0 + c + i, f);
+            else
+              part[((c0 + c + i) / 4) * kLoraTileRows + m] = f;
+          }
         }
-#pragma unroll
-        for (int i = 0; i < STEP; i += 4)
-          *reinterpret_cast<uint4*>(dst + first + c + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
       }
     }
-  }
-  tc_fence_before();
-  cluster_sync_all();
-  {
-    const float scale = s_abort ? __int_as_float(0x7fffffff) : p.scaling ? p.scaling[ad] : 1.0f;
-    constexpr int ROWS = kLoraTileRows / kLoraTileCluster;
-    for (int i = tid; i < ROWS * RP / 4; i += kLoraThreads) {
-      const int m = rank * ROWS + i / (RP / 4), r = i % (RP / 4) * 4;
-      const uint32_t part = smem_addr(s_part + m * L::LD + r);
+    tc_fence_before();  // the next tile's products come after the barrier at the top of the loop
+    if (first == last) continue;
+    fence_acq_rel_gpu();
+    __syncthreads();
+    if (tid == 0) s_last = atomicAdd(p.counters + t, 1) == last - first;
+    __syncthreads();
+    if (!s_last) continue;
+    fence_acq_rel_gpu();
+    for (int i = tid; i < L::PART_FLOATS / 4; i += kLoraThreads) {
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-      for (int c = 0; c < kLoraTileCluster; ++c) {
-        const float4 w = ld_dsmem_f4(mapa_shared(part, c));
+#pragma unroll 4
+      for (int c = first; c <= last; ++c) {
+        const float4 w = __ldcg(place(c) + i);
         v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
       }
-      uint32_t hi[2], lo[2];
-      split_bf16x2(v.x * scale, v.y * scale, hi[0], lo[0]);
-      split_bf16x2(v.z * scale, v.w * scale, hi[1], lo[1]);
-      const uint32_t at = base + (r / 64) * L::X_BYTES + m * 128 + (((r % 64) / 8 ^ (m & 7)) << 4) + (r & 4) * 2;
-#pragma unroll
-      for (int c = 0; c < kLoraTileCluster; ++c) {
-        st_dsmem_2(mapa_shared(at, c), hi[0], hi[1]);
-        st_dsmem_2(mapa_shared(at + L::H_BYTES, c), lo[0], lo[1]);
-      }
+      keep(i % kLoraTileRows, i / kLoraTileRows * 4, v);
     }
   }
-  fence_proxy_async_all();
-  cluster_sync_all();  // h is complete everywhere, and nobody touches another CTA's memory any more
-  fence_proxy_async_all();
-
-  // ---- 3. out = C + h B^T on this rank's columns
-  const __nv_bfloat16* wb = p.b + static_cast<size_t>(ad) * p.N * p.R;
-  auto load_chunk = [&](int c) {
-    const int col = (c0 + c) * 64 + piece * 8;
-    const uint32_t cs = base + L::C_RING + (c % kLoraRing) * L::X_BYTES + swizzled;
-    if (col < p.N) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (row[i] >= 0) cp_async_16_or_zero(cs + i * 32 * 128, p.C + static_cast<size_t>(row[i]) * p.N + col, true);
-    }
-    const uint32_t bs = base + L::B_RING + (c % kLoraRing) * L::B_BYTES + swizzled;
-#pragma unroll
-    for (int b = 0; b < L::KB; ++b) {
-      const int r = b * 64 + piece * 8;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int nn = (c0 + c) * 64 + row_of + 32 * i;
-        const bool in = nn < p.N && r < p.R;
-        if (r < RP)
-          cp_async_16_or_zero(bs + b * (64 * 128) + i * 32 * 128, wb + (in ? static_cast<size_t>(nn) * p.R + r : 0), in);
-      }
-    }
-  };
-  auto finish_chunk = [&](int c) {  // the chunk's product is in TMEM, its C in shared memory
-    if (ok) ok = mbar_wait(&chunk_done[c & 1], (c >> 1) & 1u, &s_abort, kLoraWaitNs);
-    tc_fence_after();
-    const int m = (warp & 3) * 32 + lane, half = warp >> 2;
-    uint32_t d[32];
-    tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (c & 1) * 64 + half * 32, d);
-    tmem_wait_ld();
-    tc_fence_before();
-    const uint32_t cs = base + L::C_RING + (c % kLoraRing) * L::X_BYTES;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t at = cs + m * 128 + (((half * 4 + j) ^ (m & 7)) << 4);
-      const uint4 v = ld_shared_16(at);
-      const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-      uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 t =
-            __floats2bfloat162_rn(__uint_as_float(in[i] << 16) + __uint_as_float(d[8 * j + 2 * i]),
-                                  __uint_as_float(in[i] & 0xFFFF0000u) + __uint_as_float(d[8 * j + 2 * i + 1]));
-        o[i] = *reinterpret_cast<const uint32_t*>(&t);
-      }
-      st_shared_16(at, make_uint4(o[0], o[1], o[2], o[3]));
-    }
-    __syncthreads();
-    const int col = (c0 + c) * 64 + piece * 8;
-    if (col < p.N) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (row[i] >= 0)
-          *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(row[i]) * p.N + col) =
-              ld_shared_16(cs + swizzled + i * 32 * 128);
-    }
-  };
-#pragma unroll 1
-  for (int c = 0; c < 2; ++c) {
-    if (c < nc) load_chunk(c);
-    cp_async_commit();
-  }
-#pragma unroll 1
-  for (int c = 0; c < nc; ++c) {
-    cp_async_wait<1>();
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (tid == 0) {
-      tc_fence_after();
-      const uint32_t d = tmem + (c & 1) * 64;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-#pragma unroll
-        for (int b = 0; b < L::KB; ++b) {
-          const uint64_t adesc = smem_desc_k128_sw128(base + half * L::H_BYTES + b * L::X_BYTES);
-          const uint64_t bdesc =
-              smem_desc_k128_sw128(base + L::B_RING + (c % kLoraRing) * L::B_BYTES + b * (64 * 128));
-#pragma unroll
-          for (int j = 0; j < (RP < 64 ? RP / 16 : 4); ++j)
-            mma_bf16(d, adesc + 2 * j, bdesc + 2 * j, idesc_bf16_f32(kLoraTileRows, 64), half + b + j > 0 ? 1u : 0u);
-        }
-      }
-      mma_commit(&chunk_done[c & 1]);
-    }
-    if (c > 0) finish_chunk(c - 1);
-    // The ring's place of chunk c - 1: its product has run, and of its C this thread overwrites only what it
-    // has itself just stored.
-    if (c + 2 < nc) load_chunk(c + 2);
-    cp_async_commit();
-  }
-  if (nc > 0) finish_chunk(nc - 1);
   cp_async_wait<0>();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, TMEM_COLS);
   if (s_abort && tid == 0) atomicCAS(p.status, 0, kLoraTimeout);
+}
+
+template <int RP>
+__global__ void __launch_bounds__(kLoraThreads, 1) lora_up_kernel(const LoraParams p) {
+  typedef LoraTile<RP> L;
+  constexpr int RING = L::RING;
+  constexpr uint32_t TMEM_COLS = 128;
+  constexpr uint32_t C_RING = 2 * L::H_BYTES, B_RING = C_RING + RING * L::X_BYTES;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t done[2];
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const int piece = tid & 7, row_of = tid >> 3;
+  const uint32_t swizzled = static_cast<uint32_t>(row_of * 128 + ((piece ^ (row_of & 7)) << 4));
+  if (tid == 0) {
+    mbar_init(&done[0], 1);
+    mbar_init(&done[1], 1);
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&s_tmem, TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  pdl_wait_prior_grid();
+  pdl_launch_dependents();
+
+  const int chunks = (p.N + 63) / 64;
+  const long long V = static_cast<long long>(p.tiles[0]) * chunks;
+  const int P = static_cast<int>(V < gridDim.x ? V : gridDim.x);
+  int v = 0, v_end = 0;
+  if (static_cast<int>(blockIdx.x) < P) {
+    v = lora_begin(blockIdx.x, P, V);
+    v_end = lora_begin(blockIdx.x + 1, P, V);
+  }
+  int row[4];
+  bool ok = true;
+  int used = 0;  // products so far: the TMEM buffer and the phase of its barrier go by it
+  while (v < v_end) {
+    const int t = v / chunks, c0 = v - t * chunks;
+    const int nc = min(chunks - c0, v_end - v);
+    const int ad = p.group[t * kLoraTileRows];
+    lora_tile_rows(p, t, row_of, row);
+    const __nv_bfloat16* wb = p.b + static_cast<size_t>(ad) * p.N * p.R;
+    auto load = [&](int c) {
+      const int col = (c0 + c) * 64 + piece * 8;
+      const uint32_t cs = base + C_RING + (c % RING) * L::X_BYTES + swizzled;
+      if (col < p.N) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (row[i] >= 0) cp_async_16_or_zero(cs + i * 32 * 128, p.C + static_cast<size_t>(row[i]) * p.N + col, true);
+      }
+      const uint32_t bs = base + B_RING + (c % RING) * L::B_BYTES + swizzled;
+#pragma unroll
+      for (int b = 0; b < L::KB; ++b) {
+        const int r = b * 64 + piece * 8;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int nn = (c0 + c) * 64 + row_of + 32 * i;
+          const bool in = nn < p.N && r < p.R;
+          if (r < RP)
+            cp_async_16_or_zero(bs + b * (64 * 128) + i * 32 * 128, wb + (in ? static_cast<size_t>(nn) * p.R + r : 0), in);
+        }
+      }
+    };
+    auto finish = [&](int c) {  // the chunk's product is on its way to TMEM, its C in shared memory
+      const int use = used + c;
+      if (ok) ok = mbar_wait(&done[use & 1], (use >> 1) & 1u, &s_abort, kLoraWaitNs);
+      tc_fence_after();
+      const int m = (warp & 3) * 32 + lane, half = warp >> 2;
+      uint32_t d[32];
+      tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (use & 1) * 64 + half * 32, d);
+      tmem_wait_ld();
+      tc_fence_before();
+      const uint32_t cs = base + C_RING + (c % RING) * L::X_BYTES;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t at = cs + m * 128 + (((half * 4 + j) ^ (m & 7)) << 4);
+        const uint4 w = ld_shared_16(at);
+        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 s =
+              __floats2bfloat162_rn(__uint_as_float(in[i] << 16) + __uint_as_float(d[8 * j + 2 * i]),
+                                    __uint_as_float(in[i] & 0xFFFF0000u) + __uint_as_float(d[8 * j + 2 * i + 1]));
+          o[i] = *reinterpret_cast<const uint32_t*>(&s);
+        }
+        st_shared_16(at, make_uint4(o[0], o[1], o[2], o[3]));
+      }
+      __syncthreads();
+      const int col = (c0 + c) * 64 + piece * 8;
+      if (col < p.N) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (row[i] >= 0)
+            *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(row[i]) * p.N + col) =
+                ld_shared_16(cs + swizzled + i * 32 * 128);
+      }
+    };
+    // h comes with the first chunk (the tile before has been finished by every thread: its last barrier)
+    const uint8_t* ht = p.h + static_cast<size_t>(t) * (2 * L::H_BYTES);
+#pragma unroll 4
+    for (int i = tid * 16; i < 2 * L::H_BYTES; i += kLoraThreads * 16) cp_async_16_or_zero(base + i, ht + i, true);
+#pragma unroll 1
+    for (int c = 0; c < RING - 1; ++c) {
+      if (c < nc) load(c);
+      cp_async_commit();
+    }
+#pragma unroll 1
+    for (int c = 0; c < nc; ++c) {
+      cp_async_wait<RING - 2>();
+      fence_proxy_async_smem();
+      __syncthreads();
+      if (tid == 0) {
+        tc_fence_after();
+        const uint32_t d = tmem + ((used + c) & 1) * 64;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int b = 0; b < L::KB; ++b) {
+            const uint64_t adesc = smem_desc_k128_sw128(base + half * L::H_BYTES + b * L::X_BYTES);
+            const uint64_t bdesc = smem_desc_k128_sw128(base + B_RING + (c % RING) * L::B_BYTES + b * (64 * 128));
+#pragma unroll
+            for (int j = 0; j < (RP < 64 ? RP / 16 : 4); ++j)
+              mma_bf16(d, adesc + 2 * j, bdesc + 2 * j, idesc_bf16_f32(kLoraTileRows, 64), half + b + j > 0 ? 1u : 0u);
+          }
+        }
+        mma_commit(&done[(used + c) & 1]);
+      }
+      if (c > 0) finish(c - 1);
+      // The ring's place of chunk c - 1: its product has run, and of its C this thread overwrites only what it
+      // has itself just stored.
+      if (c + RING - 1 < nc) load(c + RING - 1);
+      cp_async_commit();
+    }
+    finish(nc - 1);
+    used += nc;
+    v += nc;
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, TMEM_COLS);
+  if (s_abort && tid == 0) atomicCAS(p.status, 0, kLoraTimeout);
+
+  // rows without an adapter
+  if (p.out == p.C) return;
+  const int pieces = p.N / 8;
+  const long long todo = static_cast<long long>(p.tiles[1] - p.tiles[0]) * kLoraTileRows * pieces;
+  for (long long i = static_cast<long long>(blockIdx.x) * kLoraThreads + tid; i < todo;
+       i += static_cast<long long>(gridDim.x) * kLoraThreads) {
+    const int at = p.tiles[0] * kLoraTileRows + static_cast<int>(i / pieces);
+    if (p.group[at] < 0) continue;
+    const size_t src = static_cast<size_t>(p.place_row[at]) * p.N + (i % pieces) * 8;
+    *reinterpret_cast<uint4*>(p.out + src) = *reinterpret_cast<const uint4*>(p.C + src);
+  }
 }
 
 }  // namespace fg

@@ -27,6 +27,8 @@ struct LayoutParams {
   int E, chunks, M, mmax, align;  // mmax > 0: masked layout
   int* inverse;  // [M], the pair of each occupied row; nullptr: not wanted (then rows is)
   int rest;      // 1: ids outside [0, E - 1) are expert E - 1; 0: they have no row
+  int* tiles;    // with rest: blocks of `align` rows of the experts below E - 1, and of all
+  int* zeros;    // with rest: one counter per block, set to zero
 };
 
 __device__ __forceinline__ int layout_id(const LayoutParams& p, long long at) {
@@ -167,6 +169,11 @@ __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(const Layout
     if (blockIdx.x == 0)
       for (int e = threadIdx.x; e < p.E; e += kLayoutThreads) p.group[e] = min(s_count[e], p.mmax);
     return;
+  }
+  if (p.rest) {
+    const int total = s_start[p.E - 1] + (s_count[p.E - 1] + p.align - 1) / p.align * p.align;
+    if (blockIdx.x == 0 && threadIdx.x < 2) p.tiles[threadIdx.x] = (threadIdx.x ? total : s_start[p.E - 1]) / p.align;
+    for (int b = blockIdx.x * kLayoutThreads + threadIdx.x; b < p.M / p.align; b += gridDim.x * kLayoutThreads) p.zeros[b] = 0;
   }
   // m_indices: the last expert whose block starts at or before the row, if the row holds one of its
   // pairs (experts without pairs share their start with the next one and are passed over)

@@ -253,27 +253,40 @@ fg_status lora_launch(const fg::LoraParams& p, void* stream) {
 }
 
 template <int RP>
-fg_status lora_tiles_launch(const fg::LoraParams& p, int tiles, void* stream) {
-  constexpr size_t smem = fg::LoraTile<RP>::SMEM;
-  if (!allow_smem<fg::lora_tiles_kernel<RP>>(smem)) return FG_ERR_CUDA;
-  return launch(fg::lora_tiles_kernel<RP>, dim3(static_cast<unsigned>(tiles) * fg::kLoraTileCluster), fg::kLoraThreads,
-                smem, stream, fg::kLoraTileCluster, p);
+fg_status lora_tiles_launch(const fg::LoraParams& p, int sms, void* stream) {
+  typedef fg::LoraTile<RP> L;
+  if (!allow_smem<fg::lora_down_kernel<RP>>(L::DOWN_SMEM) || !allow_smem<fg::lora_up_kernel<RP>>(L::UP_SMEM))
+    return FG_ERR_CUDA;
+  const fg_status s = launch(fg::lora_down_kernel<RP>, dim3(static_cast<unsigned>(sms)), fg::kLoraThreads, L::DOWN_SMEM,
+                             stream, 1, p);
+  if (s != FG_OK) return s;
+  return launch(fg::lora_up_kernel<RP>, dim3(static_cast<unsigned>(sms)), fg::kLoraThreads, L::UP_SMEM, stream, 1, p);
 }
 
 // Many rows per adapter: tiles of 128 rows.  Few: groups of 16, found by the kernel itself.
 bool lora_by_tiles(int M, int L) { return L > 0 && L < FG_MOE_MAX_EXPERTS && M <= (1 << 24) && M > 256; }
 
-// Places of the sorted rows: tiles of the L adapters and of the rows without one.
-int lora_places(int M, int L) {
+// Scratch of the tiles: places of the sorted rows (of the L adapters and of those without), their tiles'
+// counters, h and its parts.
+struct LoraScratch {
+  int places, tiles;
+  size_t h, parts, group, hist, bytes;
+};
+LoraScratch lora_scratch(int M, int L, int R, int sms) {
+  LoraScratch s;
   const int n = M < L + 1 ? M : L + 1;
-  return fg::kLoraTileRows * (n + (M - n) / fg::kLoraTileRows);
-}
-size_t lora_scratch_bytes(int M, int L) {
-  if (!lora_by_tiles(M, L)) return 0;
-  return static_cast<size_t>(lora_places(M, L)) * 8 + layout_hist_bytes(M, L + 1);
+  s.tiles = n + (M - n) / fg::kLoraTileRows;
+  s.places = s.tiles * fg::kLoraTileRows;
+  const size_t rank = R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128;
+  s.h = 0;
+  s.parts = static_cast<size_t>(s.tiles) * 2 * (rank <= 64 ? 1 : 2) * fg::kLoraTileRows * 128;
+  s.group = s.parts + static_cast<size_t>(2) * sms * fg::kLoraTileRows * rank * 4;
+  s.hist = s.group + static_cast<size_t>(s.places) * 8 + static_cast<size_t>(s.tiles) * 4 + 8;
+  s.bytes = s.hist + layout_hist_bytes(M, L + 1);
+  return s;
 }
 
-__device__ int g_lora_status;  // FG_ERR_TIMEOUT once a wait of lora_tiles_kernel has run out
+__device__ int g_lora_status;  // FG_ERR_TIMEOUT once a wait of the kernels for many rows has run out
 
 // Its address, looked up once per device (not again during a capture).
 int* lora_status_word() {
@@ -484,7 +497,11 @@ fg_status fg_moe_combine_backward(const void* grad_out, const void* C, const int
   return launch_walk<fg::moe_combine_backward_kernel>(T, fg::kCombineGradThreads, stream, p);
 }
 
-size_t fg_lora_scratch_bytes(int M, int L) { return M > 0 && L > 0 ? lora_scratch_bytes(M, L) : 0; }
+size_t fg_lora_scratch_bytes(int M, int R, int L) {
+  if (M <= 0 || R <= 0 || L <= 0 || R > fg::kLoraMaxRank || !lora_by_tiles(M, L)) return 0;
+  const int sms = sm_count();
+  return sms > 0 ? lora_scratch(M, L, R, sms).bytes : 0;
+}
 
 fg_status fg_lora_add(const void* C, const void* x, const void* lora_a, const void* lora_b, const int* adapters,
                       const float* scaling, void* out, int M, int N, int K, int R, int L, void* scratch,
@@ -497,7 +514,7 @@ fg_status fg_lora_add(const void* C, const void* x, const void* lora_a, const vo
   if (K == 0 || R == 0) L = 0;  // no adapter adds anything
   if (L > 0 && (!x || !lora_a || !lora_b)) return FG_ERR_INVALID_ARG;
   if (!aligned(C, 16) || !aligned(x, 16) || !aligned(lora_a, 16) || !aligned(lora_b, 16) || !aligned(out, 16) ||
-      !aligned(adapters, 4) || !aligned(scaling, 4) || !aligned(scratch, 4))
+      !aligned(adapters, 4) || !aligned(scaling, 4) || !aligned(scratch, 16))
     return FG_ERR_ALIGNMENT;
   fg::LoraParams p;
   std::memset(&p, 0, sizeof(p));
@@ -514,29 +531,38 @@ fg_status fg_lora_add(const void* C, const void* x, const void* lora_a, const vo
   p.R = R;
   p.L = L;
   if (lora_by_tiles(M, L)) {
-    if (!scratch || scratch_bytes < lora_scratch_bytes(M, L)) return FG_ERR_INVALID_ARG;
+    const int sms = sm_count();
+    if (sms <= 0) return FG_ERR_CUDA;
+    const LoraScratch need = lora_scratch(M, L, R, sms);
+    if (!scratch || scratch_bytes < need.bytes) return FG_ERR_INVALID_ARG;
     p.status = lora_status_word();
     if (!p.status) return FG_ERR_CUDA;
+    uint8_t* at = static_cast<uint8_t*>(scratch);
     fg::LayoutParams lp;
     std::memset(&lp, 0, sizeof(lp));
-    lp.M = lora_places(M, L);
     lp.ids = adapters;
-    lp.group = static_cast<int*>(scratch);
-    lp.inverse = lp.group + lp.M;
-    lp.hist = lp.inverse + lp.M;
+    lp.group = reinterpret_cast<int*>(at + need.group);
+    lp.inverse = lp.group + need.places;
+    lp.tiles = lp.inverse + need.places;
+    lp.zeros = lp.tiles + 2;
+    lp.hist = reinterpret_cast<int*>(at + need.hist);
     lp.pairs = M;
     lp.E = L + 1;
+    lp.M = need.places;
     lp.align = fg::kLoraTileRows;
     lp.rest = 1;
     p.group = lp.group;
     p.place_row = lp.inverse;
+    p.tiles = lp.tiles;
+    p.counters = lp.zeros;
+    p.h = at + need.h;
+    p.parts = reinterpret_cast<float*>(at + need.parts);
     const fg_status s = layout_run(lp, stream);
     if (s != FG_OK) return s;
-    const int tiles = lp.M / fg::kLoraTileRows;
-    if (R <= 16) return lora_tiles_launch<16>(p, tiles, stream);
-    if (R <= 32) return lora_tiles_launch<32>(p, tiles, stream);
-    if (R <= 64) return lora_tiles_launch<64>(p, tiles, stream);
-    return lora_tiles_launch<128>(p, tiles, stream);
+    if (R <= 16) return lora_tiles_launch<16>(p, sms, stream);
+    if (R <= 32) return lora_tiles_launch<32>(p, sms, stream);
+    if (R <= 64) return lora_tiles_launch<64>(p, sms, stream);
+    return lora_tiles_launch<128>(p, sms, stream);
   }
   if (R <= 8) return lora_launch<1>(p, stream);
   if (R <= 16) return lora_launch<2>(p, stream);

@@ -61,9 +61,9 @@ def _beside(t, dtype, shape, device, what):
 def _apart(out: torch.Tensor, what: str, **others):
     """`out` must not share memory with any of `others`."""
     a = out.data_ptr()
-    b = a + out.numel() * out.element_size()
+    b = a + out.nbytes
     for name, t in others.items():
-        if t is not None and a < t.data_ptr() + t.numel() * t.element_size() and t.data_ptr() < b and t.numel():
+        if t is not None and t.data_ptr() < b and a < t.data_ptr() + t.nbytes and t.nbytes:
             raise ValueError(f"{what} must not overlap {name}")
 
 
@@ -313,7 +313,7 @@ def lora_add(C, x, lora_a, lora_b, adapters, scaling=None, out=None, stream=None
         return _there(dev, stream, lora_add, C, x, lora_a, lora_b, adapters, scaling, out)
     if out is None:
         out = torch.empty_like(C)
-    size = _lib.fg_lora_scratch_bytes(M, L)
+    size = _lib.fg_lora_scratch_bytes(M, R, L)
     scratch, at = _scratch(size, C)
     _check(_lib.fg_lora_add(C.data_ptr(), x_at, a_at, b_at, adapters_at, scaling_at, out.data_ptr(), M, N, K, R, L, at,
                             size, _raw_stream(dev)), "fg_lora_add")
