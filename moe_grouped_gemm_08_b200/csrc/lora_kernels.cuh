@@ -29,9 +29,7 @@ struct LoraParams {
   const int* group;      // place -> adapter (L: none, -1: padding)
   const int* place_row;  // place -> row
   const int* tiles;      // tiles of adapters, tiles in all
-  int* counters;         // per tile: parts of h written so far (zero before)
-  float* parts;          // [2 * CTAs][rank padded / 4][128][4]: parts of h
-  uint8_t* h;            // per tile: h in two bf16 halves, as tcgen05.mma reads them
+  float* parts;          // [2 * CTAs + tiles][rank padded / 4][128][4]: two parts of h per CTA, whole h per tile
   int* status;
 };
 
@@ -53,14 +51,22 @@ __device__ __forceinline__ void split_bf16x2(float v0, float v1, uint32_t& hi, u
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-// Up to 16 rows of one adapter per cluster of eight CTAs, for few rows.  Cluster m belongs to row m
+// ---------------------------------------------------------------------------- few rows
+// Up to 16 rows of one adapter per cluster of eight CTAs, one launch and no scratch.  Cluster m belongs to row m
 // and works if the row is the first of a group of 16 among the rows of its adapter.  A rank of the
 // cluster takes an eighth of K for h = A x (its warps strided over 32-wide blocks), the parts are
 // summed through distributed shared memory in rank order, and each rank then takes an eighth of N.
+// Bound by latency: the loads of a phase are all asked for before the first is used, and the first columns of
+// B and C before h is ready.
 // NT: eights of the rank held (R <= 8 NT).
 template <int NT>
-__global__ void __launch_bounds__(kLoraThreads) lora_rows_kernel(const LoraParams p) {
-  constexpr int RP = NT * 8;
+struct LoraRows {
+  static constexpr int AHEAD = NT <= 2 ? 4 : NT <= 4 ? 2 : 1;  // blocks of K asked for at once
+  static constexpr int CTAS = NT <= 4 ? 3 : 2;                 // per SM, for the registers
+};
+template <int NT>
+__global__ void __launch_bounds__(kLoraThreads, LoraRows<NT>::CTAS) lora_rows_kernel(const LoraParams p) {
+  constexpr int RP = NT * 8, AHEAD = LoraRows<NT>::AHEAD;
   extern __shared__ float s_dyn[];
   float* s_part = s_dyn;                          // [warps][16][RP], then the sum over the warps in [0]
   float* s_h = s_dyn + kLoraWarps * 16 * RP;      // [16][RP]
@@ -70,21 +76,20 @@ __global__ void __launch_bounds__(kLoraThreads) lora_rows_kernel(const LoraParam
   const int g = lane >> 2, q = lane & 3;
   const int rank = static_cast<int>(cluster_ctarank());
   const int m0 = blockIdx.x / kLoraCluster;
+  if (threadIdx.x < 16) s_rows[threadIdx.x] = -1;
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  int ad = p.adapters[m0];
-  if (ad < 0 || ad >= p.L) ad = -1;
+  auto adapter = [&](int m) {
+    const int v = p.adapters[m];
+    return v >= 0 && v < p.L ? v : -1;
+  };
+  const int ad = adapter(m0);
   if (ad < 0 && p.out == p.C) return;
   // place of row m0 among the rows of its adapter, then the rows of its group
   int before = 0;
-  for (int m = threadIdx.x; m < m0; m += kLoraThreads) {
-    const int v = p.adapters[m];
-    before += ad < 0 ? (v < 0 || v >= p.L) : v == ad;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  for (int m = threadIdx.x; m < m0; m += kLoraThreads) before += adapter(m) == ad;
+  before = __reduce_add_sync(0xffffffffu, before);
   if (lane == 0) s_cnt[warp] = before;
-  if (threadIdx.x < 16) s_rows[threadIdx.x] = -1;
   __syncthreads();
   before = 0;
 #pragma unroll
@@ -94,8 +99,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_rows_kernel(const LoraParam
   for (int base = m0; base < p.M && found < 16; base += kLoraThreads) {
     __syncthreads();
     const int m = base + threadIdx.x;
-    const int v = m < p.M ? p.adapters[m] : 0;
-    const bool mine = m < p.M && (ad < 0 ? (v < 0 || v >= p.L) : v == ad);
+    const bool mine = m < p.M && adapter(m) == ad;
     const uint32_t vote = __ballot_sync(0xffffffffu, mine);
     if (lane == 0) s_cnt[warp] = __popc(vote);
     __syncthreads();
@@ -139,33 +143,63 @@ __global__ void __launch_bounds__(kLoraThreads) lora_rows_kernel(const LoraParam
   const int k0 = static_cast<int>(static_cast<long long>(kblocks) * rank / kLoraCluster);
   const int k1 = static_cast<int>(static_cast<long long>(kblocks) * (rank + 1) / kLoraCluster);
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  const __nv_bfloat16* wa = p.a + static_cast<size_t>(ad) * p.R * p.K;
-  for (int kb = k0 + warp; kb < k1; kb += kLoraWarps) {
-    const int k = kb * 32 + q * 8;
-    const bool in = k < p.K;
-    const uint4 x0 = in && row0 >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(row0) * p.K + k)) : zero;
-    const uint4 x1 = in && row1 >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(row1) * p.K + k)) : zero;
-    uint4 w[NT];
+  const __nv_bfloat16* x0 = p.x + static_cast<size_t>(max(row0, 0)) * p.K + q * 8;
+  const __nv_bfloat16* x1 = p.x + static_cast<size_t>(max(row1, 0)) * p.K + q * 8;
+  const __nv_bfloat16* wa = p.a + (static_cast<size_t>(ad) * p.R + g) * p.K + q * 8;
+  for (int kb = k0 + warp; kb < k1; kb += kLoraWarps * AHEAD) {
+    uint4 xv[AHEAD][2], w[AHEAD][NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int r = n * 8 + g;
-      w[n] = in && r < p.R ? __ldg(reinterpret_cast<const uint4*>(wa + static_cast<size_t>(r) * p.K + k)) : zero;
+    for (int u = 0; u < AHEAD; ++u) {
+      const int k = (kb + u * kLoraWarps) * 32;
+      const bool in = kb + u * kLoraWarps < k1 && k + q * 8 < p.K;
+      xv[u][0] = in && row0 >= 0 ? __ldg(reinterpret_cast<const uint4*>(x0 + k)) : zero;
+      xv[u][1] = in && row1 >= 0 ? __ldg(reinterpret_cast<const uint4*>(x1 + k)) : zero;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        w[u][n] = in && n * 8 + g < p.R ? __ldg(reinterpret_cast<const uint4*>(wa + static_cast<size_t>(n * 8) * p.K + k)) : zero;
     }
-    const uint32_t f0[4] = {x0.x, x1.x, x0.y, x1.y}, f1[4] = {x0.z, x1.z, x0.w, x1.w};
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      mma_16816(acc[n], f0, w[n].x, w[n].y);
-      mma_16816(acc[n], f1, w[n].z, w[n].w);
+    for (int u = 0; u < AHEAD; ++u) {
+      const uint32_t f0[4] = {xv[u][0].x, xv[u][1].x, xv[u][0].y, xv[u][1].y};
+      const uint32_t f1[4] = {xv[u][0].z, xv[u][1].z, xv[u][0].w, xv[u][1].w};
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mma_16816(acc[n], f0, w[u][n].x, w[u][n].y);
+        mma_16816(acc[n], f1, w[u][n].z, w[u][n].w);
+      }
     }
   }
+  // the first columns of B and C of this warp, on their way while h is summed.  Column 8 q + 2 i + b of a
+  // 32-wide group is column 2 q + b of product i: a lane owns eight consecutive columns of two rows.
+  constexpr int NS = (NT + 1) / 2;  // 16-wide steps over the rank
+  const __nv_bfloat16* wb = p.b + static_cast<size_t>(ad) * p.N * p.R;
+  uint2 bv[4][NS];
+  uint4 cv[2];
+  auto fetch = [&](int gr) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = gr * 32 + (g >> 1) * 8 + 2 * i + (g & 1);
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const int r = s * 16 + q * 4;
+        bv[i][s] = gr < g1 && n < p.N && r < p.R
+                       ? __ldg(reinterpret_cast<const uint2*>(wb + static_cast<size_t>(n) * p.R + r))
+                       : make_uint2(0u, 0u);
+      }
+    }
+    const int col = gr * 32 + q * 8;
+    const bool in = gr < g1 && col < p.N;
+    cv[0] = in && row0 >= 0 ? *reinterpret_cast<const uint4*>(p.C + static_cast<size_t>(row0) * p.N + col) : zero;
+    cv[1] = in && row1 >= 0 ? *reinterpret_cast<const uint4*>(p.C + static_cast<size_t>(row1) * p.N + col) : zero;
+  };
+  fetch(g0 + warp);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     float* part = s_part + warp * 16 * RP + n * 8 + q * 2;
-    part[g * RP] = acc[n][0];
-    part[g * RP + 1] = acc[n][1];
-    part[(g + 8) * RP] = acc[n][2];
-    part[(g + 8) * RP + 1] = acc[n][3];
+    *reinterpret_cast<float2*>(part + g * RP) = make_float2(acc[n][0], acc[n][1]);
+    *reinterpret_cast<float2*>(part + (g + 8) * RP) = make_float2(acc[n][2], acc[n][3]);
   }
+  const float scale = p.scaling ? p.scaling[ad] : 1.0f;
   __syncthreads();
   for (int i = threadIdx.x; i < 16 * RP; i += kLoraThreads) {
     float v = 0.0f;
@@ -174,20 +208,19 @@ __global__ void __launch_bounds__(kLoraThreads) lora_rows_kernel(const LoraParam
     s_part[i] = v;
   }
   cluster_sync_all();
-  const float scale = p.scaling ? p.scaling[ad] : 1.0f;
   const uint32_t part = smem_addr(s_part);
-  for (int i = threadIdx.x; i < 16 * RP; i += kLoraThreads) {
-    float v = 0.0f;
+  for (int i = threadIdx.x; i < 16 * RP / 4; i += kLoraThreads) {
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-    for (int c = 0; c < kLoraCluster; ++c) v += ld_dsmem_f32(mapa_shared(part + i * 4, c));
-    s_h[i] = v * scale;
+    for (int c = 0; c < kLoraCluster; ++c) {
+      const float4 w = ld_dsmem_f4(mapa_shared(part + i * 16, c));
+      v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+    }
+    *reinterpret_cast<float4*>(s_h + i * 4) = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
   }
   cluster_sync_all();  // every rank has read the parts; s_h is complete
 
-  // delta = h B^T.  Both bf16 halves of h go through the tensor cores, so h keeps 16 bits.  Column
-  // 8 q + 2 i + b of a 32-wide group is column 2 q + b of product i: a lane owns eight consecutive
-  // columns of two rows.
-  constexpr int NS = (NT + 1) / 2;  // 16-wide steps over the rank
+  // delta = h B^T.  Both bf16 halves of h go through the tensor cores, so h keeps 16 bits.
   uint32_t hi[NS][4], lo[NS][4];
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
@@ -198,57 +231,51 @@ __global__ void __launch_bounds__(kLoraThreads) lora_rows_kernel(const LoraParam
       split_bf16x2(in ? s_h[row * RP + r] : 0.0f, in ? s_h[row * RP + r + 1] : 0.0f, hi[s][i], lo[s][i]);
     }
   }
-  const __nv_bfloat16* wb = p.b + static_cast<size_t>(ad) * p.N * p.R;
   for (int gr = g0 + warp; gr < g1; gr += kLoraWarps) {
     float d[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) d[i][c] = 0.0f;
-      const int n = gr * 32 + (g >> 1) * 8 + 2 * i + (g & 1);
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        const int r = s * 16 + q * 4;
-        const uint2 w = n < p.N && r < p.R ? __ldg(reinterpret_cast<const uint2*>(wb + static_cast<size_t>(n) * p.R + r))
-                                           : make_uint2(0u, 0u);
-        mma_16816(d[i], hi[s], w.x, w.y);
-        mma_16816(d[i], lo[s], w.x, w.y);
+        mma_16816(d[i], hi[s], bv[i][s].x, bv[i][s].y);
+        mma_16816(d[i], lo[s], bv[i][s].x, bv[i][s].y);
       }
     }
+    const uint4 c0 = cv[0], c1 = cv[1];
+    fetch(gr + kLoraWarps);
     const int col = gr * 32 + q * 8;
     if (col >= p.N) continue;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const int row = s ? row1 : row0;
       if (row < 0) continue;
-      const size_t at = static_cast<size_t>(row) * p.N + col;
-      const uint4 raw = *reinterpret_cast<const uint4*>(p.C + at);
-      const uint32_t c[4] = {raw.x, raw.y, raw.z, raw.w};
+      const uint32_t c[4] = {s ? c1.x : c0.x, s ? c1.y : c0.y, s ? c1.z : c0.z, s ? c1.w : c0.w};
       uint32_t o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float v0 = __uint_as_float(c[i] << 16) + d[i][2 * s];
-        const float v1 = __uint_as_float(c[i] & 0xFFFF0000u) + d[i][2 * s + 1];
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(c[i] << 16) + d[i][2 * s],
+                                                       __uint_as_float(c[i] & 0xFFFF0000u) + d[i][2 * s + 1]);
         o[i] = *reinterpret_cast<const uint32_t*>(&h);
       }
-      *reinterpret_cast<uint4*>(p.out + at) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(row) * p.N + col) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
 
 // ---------------------------------------------------------------------------- many rows
 // Rows sorted by adapter, tiles of 128 of one adapter, both products on the tensor cores, in two kernels of
-// one CTA per SM:
-//   lora_down_kernel  h = scaling x A^T.  The (tile, 64 columns of K) units are split evenly over the CTAs, so that a
+// two CTAs per SM (one above rank 64):
+//   lora_down_kernel  parts of h = x A^T.  The (tile, 64 columns of K) units are split evenly over the CTAs, so that a
 //                     few tiles more or less than SMs cost nothing; x gathered and A copied by cp.async into
-//                     128-byte-swizzled tiles, up to ten stages deep, tcgen05.mma into TMEM.  A tile that
-//                     several CTAs share is summed by the last of them, in the CTAs' order, and kept as two bf16
-//                     halves (hi + lo: 16 bits of h).
-//   lora_up_kernel    out = C + h B^T, the (tile, 64 columns of N) units split the same way: C and B by cp.async, the product
-//                     into one of two TMEM buffers while the chunk before is added and stored.
+//                     128-byte-swizzled tiles, tcgen05.mma into TMEM.
+//   lora_up_kernel    out = C + h B^T, the (tile, 64 columns of N) units split the same way.  A CTA sums the parts of its
+//                     tile's h in the order of K, scales it and keeps it as two bf16 halves (hi + lo: 16 bits of
+//                     h); C and B come by cp.async, the product goes into one of two TMEM buffers while the
+//                     chunk before is added and stored.
 // Bound by HBM: x once, C in and out.  (mma.sync took 28 us for the second product of 4096 x 4096, rank
-// 64, whose bytes take 11; one fused kernel, four CTAs of a cluster per tile, took 54 us in all.)
+// 64, whose bytes take 11; parts summed once by the last CTA of a tile took 8 us, in every reader 3.)
 constexpr int kLoraTileRows = 128;
 constexpr uint64_t kLoraWaitNs = 2000000000ull;  // far above any legal wait
 constexpr int kLoraTimeout = 6;                  // FG_ERR_TIMEOUT
@@ -259,14 +286,15 @@ struct LoraTile {
   static constexpr int KB = (RP + 63) / 64;            // 64-wide blocks of the rank
   static constexpr int X_BYTES = kLoraTileRows * 128;  // 128 rows x 64 columns
   static constexpr int STAGE_BYTES = X_BYTES + RP * 128;
-  static constexpr int STAGES = 200 * 1024 / STAGE_BYTES;
+  static constexpr int CTAS = RP <= 64 ? 2 : 1;  // per SM
+  static constexpr int STAGES = (CTAS == 2 ? 100 : 200) * 1024 / STAGE_BYTES;
   static constexpr int DOWN_SMEM = 1024 + STAGES * STAGE_BYTES;
   static constexpr int PART_FLOATS = kLoraTileRows * RP;
   static constexpr int H_BYTES = KB * X_BYTES;  // one half of h
   static constexpr int B_BYTES = KB * 64 * 128;
-  static constexpr int RING = RP <= 64 ? 7 : 4;  // chunks of C and B in shared memory
+  static constexpr int RING = RP <= 64 ? 3 : 4;  // chunks of C and B in shared memory
   static constexpr int UP_SMEM = 1024 + 2 * H_BYTES + RING * (X_BYTES + B_BYTES);
-  static_assert(DOWN_SMEM <= 225 * 1024 && UP_SMEM <= 225 * 1024, "shared memory");
+  static_assert(CTAS * (DOWN_SMEM + 1536) <= 227 * 1024 && CTAS * (UP_SMEM + 1536) <= 227 * 1024, "shared memory");
 };
 
 // Units [begin(c), begin(c + 1)) of U belong to CTA c of P; U >= P.
@@ -283,6 +311,9 @@ __device__ __forceinline__ uint4 ld_shared_16(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
+}
+__device__ __forceinline__ void st_shared_8(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 __device__ __forceinline__ void st_shared_16(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -303,6 +334,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// CTAs of lora_down_kernel's grid that have units.
+__device__ __forceinline__ int lora_down_ctas(long long U, unsigned grid) {
+  const long long most = (U + kLoraLeastUnits - 1) / kLoraLeastUnits;
+  return static_cast<int>(most < grid ? most : grid);
+}
+
 // Rows of a tile that thread `tid` copies 16 bytes of: row_of + 32 i; -1 for padding.
 __device__ __forceinline__ void lora_tile_rows(const LoraParams& p, int tile, int row_of, int (&row)[4]) {
 #pragma unroll
@@ -313,14 +350,13 @@ __device__ __forceinline__ void lora_tile_rows(const LoraParams& p, int tile, in
 }
 
 template <int RP>
-__global__ void __launch_bounds__(kLoraThreads, 1) lora_down_kernel(const LoraParams p) {
+__global__ void __launch_bounds__(kLoraThreads, LoraTile<RP>::CTAS) lora_down_kernel(const LoraParams p) {
   typedef LoraTile<RP> L;
   constexpr int STAGES = L::STAGES;
   constexpr uint32_t TMEM_COLS = RP < 32 ? 32 : RP;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t done[STAGES];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_last;
   __shared__ volatile int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -336,8 +372,7 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_down_kernel(const LoraPa
   pdl_launch_dependents();
   const int KB = (p.K + 63) / 64;
   const long long U = static_cast<long long>(p.tiles[0]) * KB;
-  const long long most = (U + kLoraLeastUnits - 1) / kLoraLeastUnits;
-  const int P = static_cast<int>(most < gridDim.x ? most : gridDim.x);
+  const int P = lora_down_ctas(U, gridDim.x);
   if (static_cast<int>(blockIdx.x) >= P) return;
   const int u0 = lora_begin(blockIdx.x, P, U), n = lora_begin(blockIdx.x + 1, P, U) - u0;
   if (warp == 0) {
@@ -349,40 +384,57 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_down_kernel(const LoraPa
   tc_fence_after();
   const uint32_t tmem = s_tmem;
 
-  int load_tile = -1, row[4];
-  const __nv_bfloat16* wa = nullptr;
-  auto load = [&](int it) {
-    const int t = (u0 + it) / KB, kb = (u0 + it) - t * KB;
-    if (t != load_tile) {
-      load_tile = t;
-      lora_tile_rows(p, t, row_of, row);
-      wa = p.a + static_cast<size_t>(p.group[t * kLoraTileRows]) * p.R * p.K;
-    }
-    const int k = kb * 64 + piece * 8;
-    const bool in = k < p.K;
-    const int at = in ? k : 0;
-    const uint32_t st = base + (it % STAGES) * L::STAGE_BYTES + swizzled;
+  // the loads run ahead of the products, over the tiles: their own tile, place in K and ring
+  int load_tile = u0 / KB, load_kb = u0 - load_tile * KB, load_stage = 0;
+  const __nv_bfloat16 *xr[4], *wr[(RP + 31) / 32];
+  bool has[4];
+  auto load_rows = [&]() {
+    int row[4];
+    lora_tile_rows(p, load_tile, row_of, row);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      cp_async_16_or_zero(st + i * 32 * 128, p.x + static_cast<size_t>(max(row[i], 0)) * p.K + at, in && row[i] >= 0);
+    for (int i = 0; i < 4; ++i) {
+      has[i] = row[i] >= 0;
+      xr[i] = p.x + static_cast<size_t>(max(row[i], 0)) * p.K + piece * 8;
+    }
+    const __nv_bfloat16* wa = p.a + static_cast<size_t>(p.group[load_tile * kLoraTileRows]) * p.R * p.K + piece * 8;
+#pragma unroll
+    for (int i = 0; i < (RP + 31) / 32; ++i) wr[i] = wa + static_cast<size_t>(min(row_of + 32 * i, p.R - 1)) * p.K;
+  };
+  load_rows();
+  auto load = [&]() {
+    const bool in = load_kb * 64 + piece * 8 < p.K;
+    const int at = in ? load_kb * 64 : -piece * 8;
+    const uint32_t st = base + load_stage * L::STAGE_BYTES + swizzled;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cp_async_16_or_zero(st + i * 32 * 128, xr[i] + at, in && has[i]);
 #pragma unroll
     for (int i = 0; i < (RP + 31) / 32; ++i) {
       const int r = row_of + 32 * i;
-      if (RP % 32 == 0 || r < RP)
-        cp_async_16_or_zero(st + L::X_BYTES + i * 32 * 128, wa + static_cast<size_t>(r < p.R ? r : 0) * p.K + at,
-                            in && r < p.R);
+      if (RP % 32 == 0 || r < RP) cp_async_16_or_zero(st + L::X_BYTES + i * 32 * 128, wr[i] + at, in && r < p.R);
     }
+    if (++load_stage == STAGES) load_stage = 0;
+  };
+  auto load_next = [&]() {  // the unit after the last one loaded
+    if (++load_kb == KB) {
+      load_kb = 0;
+      ++load_tile;
+      load_rows();
+    }
+    load();
   };
   bool ok = true;
 #pragma unroll 1
   for (int it = 0; it < STAGES - 1; ++it) {
-    if (it < n) load(it);
+    if (it == 0)
+      load();
+    else if (it < n)
+      load_next();
     cp_async_commit();
   }
+  int t = u0 / KB, kb = u0 - t * KB;
+  bool fresh = true;  // the first unit of its tile here
 #pragma unroll 1
   for (int it = 0; it < n; ++it) {
-    const int u = u0 + it, t = u / KB, kb = u - t * KB;
-    const int from = max(t * KB, u0);  // the first unit of this tile here
     cp_async_wait<STAGES - 2>();
     fence_proxy_async_smem();
     __syncthreads();
@@ -392,44 +444,38 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_down_kernel(const LoraPa
       const uint64_t adesc = smem_desc_k128_sw128(st), bdesc = smem_desc_k128_sw128(st + L::X_BYTES);
 #pragma unroll
       for (int j = 0; j < 4; ++j)  // 16 values = 32 bytes = 2 descriptor units per step
-        mma_bf16(tmem, adesc + 2 * j, bdesc + 2 * j, idesc_bf16_f32(kLoraTileRows, RP), u > from || j > 0 ? 1u : 0u);
+        mma_bf16(tmem, adesc + 2 * j, bdesc + 2 * j, idesc_bf16_f32(kLoraTileRows, RP), !fresh || j > 0 ? 1u : 0u);
       mma_commit(&done[it % STAGES]);
     }
     const int next = it + STAGES - 1;
     if (next < n) {
       if (it > 0 && ok)  // the products that read this place of the ring
         ok = mbar_wait(&done[next % STAGES], ((it - 1) / STAGES) & 1u, &s_abort, kLoraWaitNs);
-      if (ok) load(next);
+      if (ok) load_next();
     }
     cp_async_commit();
-    if (kb < KB - 1 && it < n - 1) continue;
+    fresh = false;
+    if (kb < KB - 1 && it < n - 1) {
+      ++kb;
+      continue;
+    }
 
     // the tile ends here, or this CTA's share of it does
     if (ok) ok = mbar_wait(&done[it % STAGES], (it / STAGES) & 1u, &s_abort, kLoraWaitNs);
     tc_fence_after();
-    const int first = lora_owner(t * KB, P, U), last = lora_owner(t * KB + KB - 1, P, U);
-    const int ad = p.group[t * kLoraTileRows];
-    const float scale = s_abort ? __int_as_float(0x7fffffff) : p.scaling ? p.scaling[ad] : 1.0f;
-    uint8_t* ht = p.h + static_cast<size_t>(t) * (2 * L::H_BYTES);
-    auto keep = [&](int m, int r, float4 v) {  // h[m][r .. r + 3] as two halves
-      uint32_t hi[2], lo[2];
-      split_bf16x2(v.x * scale, v.y * scale, hi[0], lo[0]);
-      split_bf16x2(v.z * scale, v.w * scale, hi[1], lo[1]);
-      uint8_t* at = ht + (r / 64) * L::X_BYTES + m * 128 + ((((r % 64) / 8) ^ (m & 7)) << 4) + (r & 4) * 2;
-      *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(at + L::H_BYTES) = make_uint2(lo[0], lo[1]);
-    };
-    // of the CTA's two places for parts, the first is for a tile that began in an earlier CTA
-    auto place = [&](int c) {
-      return reinterpret_cast<float4*>(p.parts + static_cast<size_t>(2 * c + (lora_begin(c, P, U) > t * KB ? 0 : 1)) *
-                                                     L::PART_FLOATS);
-    };
+    // a whole tile has a place of its own; of a CTA's two places for parts, the second is for the tile that
+    // begins in it, the first for one that began in an earlier CTA
+    const bool begins = t * KB >= u0, ends = kb == KB - 1;
+    const int place = begins && ends ? 2 * gridDim.x + t : 2 * blockIdx.x + (begins ? 1 : 0);
+    float4* part = reinterpret_cast<float4*>(p.parts + static_cast<size_t>(place) * L::PART_FLOATS);
+    fresh = true;
+    kb = 0;
+    ++t;
     {
       constexpr int CPW = RP >= 32 ? RP / 2 : RP;
       constexpr int STEP = CPW < 32 ? 16 : 32;
       const int c0 = (warp >> 2) * CPW, m = (warp & 3) * 32 + lane;
       if (c0 < RP) {
-        float4* part = place(blockIdx.x);
 #pragma unroll
         for (int c = 0; c < CPW; c += STEP) {
           uint32_t v[STEP];
@@ -441,33 +487,15 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_down_kernel(const LoraPa
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < STEP; i += 4) {
-            const float4 f = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]),
-                                         __uint_as_float(v[i + 3]));
-            if (first == last)
-              keep(m, c0 + c + i, f);
-            else
-              part[((c0 + c + i) / 4) * kLoraTileRows + m] = f;
+            const uint32_t poison = s_abort ? 0x7fffffffu : 0u;  // NaN after a wait that ran out
+            part[((c0 + c + i) / 4) * kLoraTileRows + m] =
+                make_float4(__uint_as_float(v[i] | poison), __uint_as_float(v[i + 1] | poison),
+                            __uint_as_float(v[i + 2] | poison), __uint_as_float(v[i + 3] | poison));
           }
         }
       }
     }
     tc_fence_before();  // the next tile's products come after the barrier at the top of the loop
-    if (first == last) continue;
-    fence_acq_rel_gpu();
-    __syncthreads();
-    if (tid == 0) s_last = atomicAdd(p.counters + t, 1) == last - first;
-    __syncthreads();
-    if (!s_last) continue;
-    fence_acq_rel_gpu();
-    for (int i = tid; i < L::PART_FLOATS / 4; i += kLoraThreads) {
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-      for (int c = first; c <= last; ++c) {
-        const float4 w = __ldcg(place(c) + i);
-        v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
-      }
-      keep(i % kLoraTileRows, i / kLoraTileRows * 4, v);
-    }
   }
   cp_async_wait<0>();
   __syncthreads();
@@ -476,7 +504,7 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_down_kernel(const LoraPa
 }
 
 template <int RP>
-__global__ void __launch_bounds__(kLoraThreads, 1) lora_up_kernel(const LoraParams p) {
+__global__ void __launch_bounds__(kLoraThreads, LoraTile<RP>::CTAS) lora_up_kernel(const LoraParams p) {
   typedef LoraTile<RP> L;
   constexpr int RING = L::RING;
   constexpr uint32_t TMEM_COLS = 128;
@@ -503,10 +531,13 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_up_kernel(const LoraPara
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  pdl_wait_prior_grid();
-  pdl_launch_dependents();
 
+  // The preceding kernel, lora_down_kernel, let this one start after it had waited for all before it: only the
+  // parts of h, and what is written, come after the wait below.
   const int chunks = (p.N + 63) / 64;
+  const int KB = (p.K + 63) / 64;
+  const long long U = static_cast<long long>(p.tiles[0]) * KB;
+  const int PU = lora_down_ctas(U, gridDim.x);  // the grid of lora_down_kernel, as large as this one
   const long long V = static_cast<long long>(p.tiles[0]) * chunks;
   const int P = static_cast<int>(V < gridDim.x ? V : gridDim.x);
   int v = 0, v_end = 0;
@@ -515,7 +546,7 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_up_kernel(const LoraPara
     v_end = lora_begin(blockIdx.x + 1, P, V);
   }
   int row[4];
-  bool ok = true;
+  bool ok = true, waited = false;
   int used = 0;  // products so far: the TMEM buffer and the phase of its barrier go by it
   while (v < v_end) {
     const int t = v / chunks, c0 = v - t * chunks;
@@ -579,14 +610,49 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_up_kernel(const LoraPara
                 ld_shared_16(cs + swizzled + i * 32 * 128);
       }
     };
-    // h comes with the first chunk (the tile before has been finished by every thread: its last barrier)
-    const uint8_t* ht = p.h + static_cast<size_t>(t) * (2 * L::H_BYTES);
-#pragma unroll 4
-    for (int i = tid * 16; i < 2 * L::H_BYTES; i += kLoraThreads * 16) cp_async_16_or_zero(base + i, ht + i, true);
 #pragma unroll 1
     for (int c = 0; c < RING - 1; ++c) {
       if (c < nc) load(c);
       cp_async_commit();
+    }
+    if (!waited) {
+      waited = true;
+      pdl_wait_prior_grid();
+      pdl_launch_dependents();
+    }
+    {  // h (its last product of the tile before has run: every thread has waited for it)
+      const int first = lora_owner(t * KB, PU, U), last = lora_owner(t * KB + KB - 1, PU, U);
+      const float scale = p.scaling ? p.scaling[ad] : 1.0f;
+      constexpr int EACH = L::PART_FLOATS / 4 / kLoraThreads, SIDE = EACH < 8 ? EACH : 8;  // quads of a thread; at once
+#pragma unroll 1
+      for (int e = 0; e < EACH; e += SIDE) {
+        float4 h[SIDE];
+#pragma unroll
+        for (int i = 0; i < SIDE; ++i) h[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+        for (int c = first; c <= last; ++c) {
+          const int place = first == last ? 2 * gridDim.x + t : 2 * c + (c == first ? 1 : 0);
+          const float4* part = reinterpret_cast<const float4*>(p.parts + static_cast<size_t>(place) * L::PART_FLOATS) +
+                               e * kLoraThreads + tid;
+          float4 w[SIDE];
+#pragma unroll
+          for (int i = 0; i < SIDE; ++i) w[i] = __ldcg(part + i * kLoraThreads);
+#pragma unroll
+          for (int i = 0; i < SIDE; ++i)
+            h[i] = make_float4(h[i].x + w[i].x, h[i].y + w[i].y, h[i].z + w[i].z, h[i].w + w[i].w);
+        }
+#pragma unroll
+        for (int i = 0; i < SIDE; ++i) {
+          const int at = (e + i) * kLoraThreads + tid, m = at % kLoraTileRows, r = at / kLoraTileRows * 4;
+          uint32_t hi[2], lo[2];
+          split_bf16x2(h[i].x * scale, h[i].y * scale, hi[0], lo[0]);
+          split_bf16x2(h[i].z * scale, h[i].w * scale, hi[1], lo[1]);
+          const uint32_t dst =
+              base + (r / 64) * L::X_BYTES + m * 128 + ((((r % 64) / 8) ^ (m & 7)) << 4) + (r & 4) * 2;
+          st_shared_8(dst, hi[0], hi[1]);
+          st_shared_8(dst + L::H_BYTES, lo[0], lo[1]);
+        }
+      }
     }
 #pragma unroll 1
     for (int c = 0; c < nc; ++c) {
@@ -618,6 +684,10 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_up_kernel(const LoraPara
     finish(nc - 1);
     used += nc;
     v += nc;
+  }
+  if (!waited) {
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
   }
   cp_async_wait<0>();
   __syncthreads();

@@ -13,8 +13,6 @@
 
 namespace fg {
 
-constexpr int kLayoutThreads = 256;
-constexpr int kLayoutWarps = kLayoutThreads / 32;
 constexpr int kLayoutMaxExperts = 1024;
 constexpr int kRowsMaxK = 32;
 
@@ -28,7 +26,6 @@ struct LayoutParams {
   int* inverse;  // [M], the pair of each occupied row; nullptr: not wanted (then rows is)
   int rest;      // 1: ids outside [0, E - 1) are expert E - 1; 0: they have no row
   int* tiles;    // with rest: blocks of `align` rows of the experts below E - 1, and of all
-  int* zeros;    // with rest: one counter per block, set to zero
 };
 
 __device__ __forceinline__ int layout_id(const LayoutParams& p, long long at) {
@@ -37,54 +34,57 @@ __device__ __forceinline__ int layout_id(const LayoutParams& p, long long at) {
   return id >= 0 && id < p.E - p.rest ? id : none;
 }
 
-// Counts per expert of one chunk of pairs (kLayoutThreads * ITEMS, in their order).
-template <int ITEMS>
-__global__ void __launch_bounds__(kLayoutThreads) moe_layout_count_kernel(const LayoutParams p) {
+// Counts per expert of one chunk of pairs (THREADS * ITEMS, in their order).
+template <int THREADS, int ITEMS>
+__global__ void __launch_bounds__(THREADS) moe_layout_count_kernel(const LayoutParams p) {
   __shared__ int s_cnt[kLayoutMaxExperts];
-  for (int e = threadIdx.x; e < p.E; e += kLayoutThreads) s_cnt[e] = 0;
+  for (int e = threadIdx.x; e < p.E; e += THREADS) s_cnt[e] = 0;
   __syncthreads();
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  const long long base = static_cast<long long>(blockIdx.x) * (kLayoutThreads * ITEMS);
+  const long long base = static_cast<long long>(blockIdx.x) * (THREADS * ITEMS);
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
-    const long long at = base + i * kLayoutThreads + threadIdx.x;
+    const long long at = base + i * THREADS + threadIdx.x;
     const int id = layout_id(p, at);
     if (id >= 0) atomicAdd(&s_cnt[id], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += kLayoutThreads)
+  for (int e = threadIdx.x; e < p.E; e += THREADS)
     p.hist[static_cast<size_t>(blockIdx.x) * p.E + e] = s_cnt[e];
 }
 
-// The stable counting sort of a chunk: a pair's row is its expert's first row, plus the expert's
+// More CTAs than chunks help to fill m_indices: with one chunk all of them count it, with several they
+// read the counts; only the chunk's own CTA writes its rows.  The stable counting sort of a chunk: a pair's row is its expert's first row, plus the expert's
 // pairs in earlier chunks, in earlier warps of the chunk, and earlier in its warp.
-template <int ITEMS>
-__global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(const LayoutParams p) {
-  __shared__ uint16_t s_warp[kLayoutWarps][kLayoutMaxExperts];  // counts, then prefixes over the warps
+template <int THREADS, int ITEMS>
+__global__ void __launch_bounds__(THREADS) moe_layout_kernel(const LayoutParams p) {
+  constexpr int WARPS = THREADS / 32;
+  extern __shared__ uint16_t s_warp_counts[];  // [WARPS][E]: counts, then prefixes over the warps
   __shared__ int s_start[kLayoutMaxExperts];   // the expert's first row
   __shared__ int s_count[kLayoutMaxExperts];   // its pairs
   __shared__ int s_before[kLayoutMaxExperts];  // its pairs in earlier chunks
-  __shared__ int s_scan[kLayoutWarps];
+  __shared__ int s_scan[WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = threadIdx.x; e < p.E; e += kLayoutThreads) {
+  for (int e = threadIdx.x; e < p.E; e += THREADS) {
 #pragma unroll
-    for (int w = 0; w < kLayoutWarps; ++w) s_warp[w][e] = 0;
+    for (int w = 0; w < WARPS; ++w) s_warp_counts[w * p.E + e] = 0;
     s_before[e] = 0;
     s_count[e] = 0;
   }
   __syncthreads();
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  const long long base = static_cast<long long>(blockIdx.x) * (kLayoutThreads * ITEMS) + warp * 32 * ITEMS;
+  const int chunk = p.chunks > 1 ? blockIdx.x : 0;
+  const long long base = static_cast<long long>(chunk) * (THREADS * ITEMS) + warp * 32 * ITEMS;
   int id[ITEMS], rank[ITEMS];
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     id[i] = layout_id(p, base + i * 32 + lane);
   }
   if (p.chunks > 1) {  // all threads over (chunk, expert), as many chunks side by side as there is room
-    const int cols = p.E < 32 ? 32 : p.E < kLayoutThreads ? (p.E + 31) / 32 * 32 : kLayoutThreads;
-    const int parts = kLayoutThreads / cols;
+    const int cols = p.E < 32 ? 32 : p.E < THREADS ? (p.E + 31) / 32 * 32 : THREADS;
+    const int parts = THREADS / cols;
     const int part = threadIdx.x / cols;
     for (int e = threadIdx.x % cols; e < p.E && part < parts; e += cols) {
       int before = 0, count = 0;
@@ -102,19 +102,19 @@ __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(const Layout
   for (int i = 0; i < ITEMS; ++i) {
     const int e = id[i];
     const uint32_t same = __match_any_sync(0xffffffffu, e);
-    const int before = e >= 0 ? s_warp[warp][e] : 0;
+    const int before = e >= 0 ? s_warp_counts[warp * p.E + e] : 0;
     rank[i] = before + __popc(same & ((1u << lane) - 1));
     __syncwarp();
-    if (e >= 0 && lane == __ffs(same) - 1) s_warp[warp][e] = static_cast<uint16_t>(before + __popc(same));
+    if (e >= 0 && lane == __ffs(same) - 1) s_warp_counts[warp * p.E + e] = static_cast<uint16_t>(before + __popc(same));
     __syncwarp();
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += kLayoutThreads) {
+  for (int e = threadIdx.x; e < p.E; e += THREADS) {
     int run = 0;
 #pragma unroll
-    for (int w = 0; w < kLayoutWarps; ++w) {
-      const int c = s_warp[w][e];
-      s_warp[w][e] = static_cast<uint16_t>(run);
+    for (int w = 0; w < WARPS; ++w) {
+      const int c = s_warp_counts[w * p.E + e];
+      s_warp_counts[w * p.E + e] = static_cast<uint16_t>(run);
       run += c;
     }
     if (p.chunks <= 1) s_count[e] = run;
@@ -122,9 +122,9 @@ __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(const Layout
   __syncthreads();
   // first rows: the experts' blocks one after the other, each padded to the alignment
   if (p.mmax > 0) {
-    for (int e = threadIdx.x; e < p.E; e += kLayoutThreads) s_start[e] = e * p.mmax;
+    for (int e = threadIdx.x; e < p.E; e += THREADS) s_start[e] = e * p.mmax;
   } else {
-    constexpr int PER = kLayoutMaxExperts / kLayoutThreads;
+    constexpr int PER = kLayoutMaxExperts / THREADS;
     int pad[PER], sum = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -153,11 +153,11 @@ __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(const Layout
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     const long long at = base + i * 32 + lane;
-    if (at >= p.pairs) continue;
+    if (at >= p.pairs || (p.chunks <= 1 && blockIdx.x > 0)) continue;
     const int e = id[i];
     int row = -1;
     if (e >= 0) {
-      const int place = s_before[e] + s_warp[warp][e] + rank[i];
+      const int place = s_before[e] + s_warp_counts[warp * p.E + e] + rank[i];
       if (p.mmax <= 0 || place < p.mmax) row = s_start[e] + place;
     }
     if (p.inverse)
@@ -167,23 +167,26 @@ __global__ void __launch_bounds__(kLayoutThreads) moe_layout_kernel(const Layout
   }
   if (p.mmax > 0) {
     if (blockIdx.x == 0)
-      for (int e = threadIdx.x; e < p.E; e += kLayoutThreads) p.group[e] = min(s_count[e], p.mmax);
+      for (int e = threadIdx.x; e < p.E; e += THREADS) p.group[e] = min(s_count[e], p.mmax);
     return;
   }
-  if (p.rest) {
+  if (p.rest && blockIdx.x == 0 && threadIdx.x < 2) {
     const int total = s_start[p.E - 1] + (s_count[p.E - 1] + p.align - 1) / p.align * p.align;
-    if (blockIdx.x == 0 && threadIdx.x < 2) p.tiles[threadIdx.x] = (threadIdx.x ? total : s_start[p.E - 1]) / p.align;
-    for (int b = blockIdx.x * kLayoutThreads + threadIdx.x; b < p.M / p.align; b += gridDim.x * kLayoutThreads) p.zeros[b] = 0;
+    p.tiles[threadIdx.x] = (threadIdx.x ? total : s_start[p.E - 1]) / p.align;
   }
-  // m_indices: the last expert whose block starts at or before the row, if the row holds one of its
-  // pairs (experts without pairs share their start with the next one and are passed over)
-  for (int r = blockIdx.x * kLayoutThreads + threadIdx.x; r < p.M; r += gridDim.x * kLayoutThreads) {
+  // m_indices, four rows at a time (a block is a multiple of four): the last expert whose block starts at or
+  // before the row, if the row holds one of its pairs (experts without pairs share their start with the
+  // next one and are passed over)
+  for (int r = (blockIdx.x * THREADS + threadIdx.x) * 4; r < p.M; r += gridDim.x * THREADS * 4) {
     int lo = 0, hi = p.E;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (s_start[mid] <= r) lo = mid; else hi = mid;
     }
-    p.group[r] = r - s_start[lo] < s_count[lo] ? lo : -1;
+    const int left = s_start[lo] + s_count[lo] - r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (r + i < p.M) p.group[r + i] = i < left ? lo : -1;
   }
 }
 

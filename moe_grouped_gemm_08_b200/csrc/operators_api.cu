@@ -190,24 +190,37 @@ size_t route_scratch_bytes(int S, int E, const RouteSplit& r) {
 }
 
 // ------------------------------------------------------------------------------------ row layouts
-// Pairs per thread: 2 while that leaves a CTA per SM or fewer, else 8; one CTA (and one launch) up to 2048.
-int layout_items(long long pairs) {
-  const long long two = 2 * fg::kLayoutThreads;
-  return pairs <= two || (pairs > 4 * two && pairs <= 148 * two) ? 2 : 8;
+// How the pairs are split: one chunk (and one launch) up to 2048, then 512 a chunk while that leaves a CTA per
+// SM or fewer, else 2048.  (4096 pairs of 8 experts: 4.7 us in eight chunks, 5.9 us in one.)
+struct LayoutSplit {
+  int threads, items;
+};
+LayoutSplit layout_split(long long pairs) {
+  if (pairs <= 512) return {256, 2};
+  if (pairs <= 2048) return {1024, 2};
+  if (pairs <= 148 * 512) return {256, 2};
+  return {256, 8};
 }
 int layout_chunks(long long pairs) {
-  return static_cast<int>(cdiv(pairs, static_cast<long long>(layout_items(pairs)) * fg::kLayoutThreads));
+  const LayoutSplit s = layout_split(pairs);
+  return static_cast<int>(cdiv(pairs, static_cast<long long>(s.threads) * s.items));
 }
 
-template <int ITEMS>
+template <int THREADS, int ITEMS>
 fg_status layout_launch(const fg::LayoutParams& p, void* stream) {
+  constexpr size_t most = THREADS / 32 * fg::kLayoutMaxExperts * 2;
+  const size_t smem = static_cast<size_t>(THREADS / 32) * p.E * 2;
+  if (!allow_smem<fg::moe_layout_kernel<THREADS, ITEMS>>(most)) return FG_ERR_CUDA;
   if (p.chunks > 1) {
-    const fg_status s = launch(fg::moe_layout_count_kernel<ITEMS>, dim3(p.chunks), fg::kLayoutThreads, 0, stream, 1, p);
+    const fg_status s = launch(fg::moe_layout_count_kernel<THREADS, ITEMS>, dim3(p.chunks), THREADS, 0, stream, 1, p);
     if (s != FG_OK) return s;
   }
-  return launch(fg::moe_layout_kernel<ITEMS>, dim3(p.chunks > 0 ? p.chunks : 1), fg::kLayoutThreads, 0, stream, 1, p);
+  // a CTA per chunk, and at least one per 4096 rows of m_indices (256 experts, 512 pairs: 51 us with one)
+  const long long fill = cdiv(p.M, 4096);
+  long long ctas = p.chunks > fill ? p.chunks : fill < 128 ? fill : 128;
+  if (ctas < 1) ctas = 1;
+  return launch(fg::moe_layout_kernel<THREADS, ITEMS>, dim3(static_cast<unsigned>(ctas)), THREADS, smem, stream, 1, p);
 }
-
 size_t layout_hist_bytes(long long pairs, int E) {
   const int chunks = layout_chunks(pairs);
   return chunks > 1 ? static_cast<size_t>(chunks) * E * 4 : 0;
@@ -215,7 +228,9 @@ size_t layout_hist_bytes(long long pairs, int E) {
 
 fg_status layout_run(fg::LayoutParams& p, void* stream) {
   p.chunks = layout_chunks(p.pairs);
-  return layout_items(p.pairs) == 2 ? layout_launch<2>(p, stream) : layout_launch<8>(p, stream);
+  const LayoutSplit s = layout_split(p.pairs);
+  if (s.threads == 1024) return layout_launch<1024, 2>(p, stream);
+  return s.items == 2 ? layout_launch<256, 2>(p, stream) : layout_launch<256, 8>(p, stream);
 }
 
 fg_status layout_call(const int* ids, int* rows, int* group, long long pairs, int E, int M, int mmax, void* scratch,
@@ -257,20 +272,19 @@ fg_status lora_tiles_launch(const fg::LoraParams& p, int sms, void* stream) {
   typedef fg::LoraTile<RP> L;
   if (!allow_smem<fg::lora_down_kernel<RP>>(L::DOWN_SMEM) || !allow_smem<fg::lora_up_kernel<RP>>(L::UP_SMEM))
     return FG_ERR_CUDA;
-  const fg_status s = launch(fg::lora_down_kernel<RP>, dim3(static_cast<unsigned>(sms)), fg::kLoraThreads, L::DOWN_SMEM,
-                             stream, 1, p);
+  const dim3 grid(static_cast<unsigned>(sms * L::CTAS));
+  const fg_status s = launch(fg::lora_down_kernel<RP>, grid, fg::kLoraThreads, L::DOWN_SMEM, stream, 1, p);
   if (s != FG_OK) return s;
-  return launch(fg::lora_up_kernel<RP>, dim3(static_cast<unsigned>(sms)), fg::kLoraThreads, L::UP_SMEM, stream, 1, p);
+  return launch(fg::lora_up_kernel<RP>, grid, fg::kLoraThreads, L::UP_SMEM, stream, 1, p);
 }
 
 // Many rows per adapter: tiles of 128 rows.  Few: groups of 16, found by the kernel itself.
 bool lora_by_tiles(int M, int L) { return L > 0 && L < FG_MOE_MAX_EXPERTS && M <= (1 << 24) && M > 256; }
 
-// Scratch of the tiles: places of the sorted rows (of the L adapters and of those without), their tiles'
-// counters, h and its parts.
+// Scratch of the tiles: parts of h, then the places of the sorted rows (of the L adapters and of those without).
 struct LoraScratch {
   int places, tiles;
-  size_t h, parts, group, hist, bytes;
+  size_t group, hist, bytes;
 };
 LoraScratch lora_scratch(int M, int L, int R, int sms) {
   LoraScratch s;
@@ -278,10 +292,9 @@ LoraScratch lora_scratch(int M, int L, int R, int sms) {
   s.tiles = n + (M - n) / fg::kLoraTileRows;
   s.places = s.tiles * fg::kLoraTileRows;
   const size_t rank = R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128;
-  s.h = 0;
-  s.parts = static_cast<size_t>(s.tiles) * 2 * (rank <= 64 ? 1 : 2) * fg::kLoraTileRows * 128;
-  s.group = s.parts + static_cast<size_t>(2) * sms * fg::kLoraTileRows * rank * 4;
-  s.hist = s.group + static_cast<size_t>(s.places) * 8 + static_cast<size_t>(s.tiles) * 4 + 8;
+  const int ctas = sms * (rank <= 64 ? fg::LoraTile<64>::CTAS : fg::LoraTile<128>::CTAS);
+  s.group = static_cast<size_t>(2 * ctas + s.tiles) * fg::kLoraTileRows * rank * 4;
+  s.hist = s.group + static_cast<size_t>(s.places) * 8 + 8;
   s.bytes = s.hist + layout_hist_bytes(M, L + 1);
   return s;
 }
@@ -544,7 +557,6 @@ fg_status fg_lora_add(const void* C, const void* x, const void* lora_a, const vo
     lp.group = reinterpret_cast<int*>(at + need.group);
     lp.inverse = lp.group + need.places;
     lp.tiles = lp.inverse + need.places;
-    lp.zeros = lp.tiles + 2;
     lp.hist = reinterpret_cast<int*>(at + need.hist);
     lp.pairs = M;
     lp.E = L + 1;
@@ -554,9 +566,7 @@ fg_status fg_lora_add(const void* C, const void* x, const void* lora_a, const vo
     p.group = lp.group;
     p.place_row = lp.inverse;
     p.tiles = lp.tiles;
-    p.counters = lp.zeros;
-    p.h = at + need.h;
-    p.parts = reinterpret_cast<float*>(at + need.parts);
+    p.parts = reinterpret_cast<float*>(at);
     const fg_status s = layout_run(lp, stream);
     if (s != FG_OK) return s;
     if (R <= 16) return lora_tiles_launch<16>(p, sms, stream);

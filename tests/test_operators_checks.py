@@ -61,7 +61,7 @@ def test_layout_argument_errors():
     assert con(P, P, P, 10, 0, 512, NULL, 0, NULL) == 1
     assert con(P, P, P, -1, 4, 512, NULL, 0, NULL) == 1
     assert con(P, P, P, 10, 4, 511, NULL, 0, NULL) == 1      # fewer rows than a choice may take
-    assert con(P, P, P, 5000, 4, 8192, NULL, 0, NULL) == 1   # scratch needed
+    assert con(P, P, P, 10000, 4, 16384, NULL, 0, NULL) == 1  # scratch needed
     assert con(P, P, P, 10, 1025, BIG % (1 << 31), NULL, 0, NULL) == 3
     assert con(P, P, P, (1 << 24) + 1, 4, 1 << 26, P, BIG, NULL) == 3
     assert con(P + 2, P, P, 10, 4, 512, NULL, 0, NULL) == 2
