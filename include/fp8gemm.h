@@ -310,7 +310,7 @@ fg_status fg_moe_combine_backward(const void* grad_out, const void* C, const int
  * x bf16 [M][K], lora_a bf16 [L][R][K], lora_b bf16 [L][N][R], scaling fp32 [L] or NULL (all 1).
  * Both products accumulate in fp32, A_a x is kept to 16 bits of mantissa between them, and the sum
  * is rounded once.  K % 16 == 0, N % 8 == 0, R % 8 == 0, R <= 128 (a smaller rank is padded with
- * zeros).  Rows of one adapter may stand anywhere; many rows are first sorted by adapter, which
+ * zeros), M <= 2^24.  Rows of one adapter may stand anywhere; many rows are first sorted by adapter, which
  * takes the scratch (16-byte aligned).  The first call on a device is made outside stream capture.
  * A wait of a kernel for many rows that runs out (about two seconds) makes it write NaN and leave
  * FG_ERR_TIMEOUT for fg_lora_status, which synchronises `stream`, reads and clears it. */

@@ -13,7 +13,6 @@ namespace fg {
 
 constexpr int kLoraThreads = 256;
 constexpr int kLoraWarps = kLoraThreads / 32;
-constexpr int kLoraCluster = 8;
 constexpr int kLoraMaxRank = 128;
 
 struct LoraParams {
@@ -52,19 +51,19 @@ __device__ __forceinline__ void split_bf16x2(float v0, float v1, uint32_t& hi, u
 }
 
 // ---------------------------------------------------------------------------- few rows
-// Up to 16 rows of one adapter per cluster of eight CTAs, one launch and no scratch.  Cluster m belongs to row m
+// Up to 16 rows of one adapter per cluster of CL CTAs, one launch and no scratch.  Cluster m belongs to row m
 // and works if the row is the first of a group of 16 among the rows of its adapter.  A rank of the
-// cluster takes an eighth of K for h = A x (its warps strided over 32-wide blocks), the parts are
-// summed through distributed shared memory in rank order, and each rank then takes an eighth of N.
+// cluster takes a CL-th of K for h = A x (its warps strided over 32-wide blocks), the parts are
+// summed through distributed shared memory in rank order, and each rank then takes a CL-th of N.
 // Bound by latency: the loads of a phase are all asked for before the first is used, and the first columns of
 // B and C before h is ready.
 // NT: eights of the rank held (R <= 8 NT).
 template <int NT>
 struct LoraRows {
   static constexpr int AHEAD = NT <= 2 ? 4 : NT <= 4 ? 2 : 1;  // blocks of K asked for at once
-  static constexpr int CTAS = NT <= 4 ? 3 : 2;                 // per SM, for the registers
+  static constexpr int CTAS = NT <= 4 ? 3 : NT <= 8 ? 2 : 1;   // per SM, for the registers
 };
-template <int NT>
+template <int NT, int CL>
 __global__ void __launch_bounds__(kLoraThreads, LoraRows<NT>::CTAS) lora_rows_kernel(const LoraParams p) {
   constexpr int RP = NT * 8, AHEAD = LoraRows<NT>::AHEAD;
   extern __shared__ float s_dyn[];
@@ -75,7 +74,7 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRows<NT>::CTAS) lora_rows_ke
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q = lane & 3;
   const int rank = static_cast<int>(cluster_ctarank());
-  const int m0 = blockIdx.x / kLoraCluster;
+  const int m0 = blockIdx.x / CL;
   if (threadIdx.x < 16) s_rows[threadIdx.x] = -1;
   pdl_wait_prior_grid();
   pdl_launch_dependents();
@@ -114,8 +113,8 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRows<NT>::CTAS) lora_rows_ke
   __syncthreads();
   const int row0 = s_rows[g], row1 = s_rows[g + 8];
   const int groups = (p.N + 31) / 32;
-  const int g0 = static_cast<int>(static_cast<long long>(groups) * rank / kLoraCluster);
-  const int g1 = static_cast<int>(static_cast<long long>(groups) * (rank + 1) / kLoraCluster);
+  const int g0 = static_cast<int>(static_cast<long long>(groups) * rank / CL);
+  const int g1 = static_cast<int>(static_cast<long long>(groups) * (rank + 1) / CL);
 
   if (ad < 0) {  // no adapter: the rows are copied
     for (int gr = g0 + warp; gr < g1; gr += kLoraWarps) {
@@ -140,8 +139,8 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRows<NT>::CTAS) lora_rows_ke
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
   const int kblocks = (p.K + 31) / 32;
-  const int k0 = static_cast<int>(static_cast<long long>(kblocks) * rank / kLoraCluster);
-  const int k1 = static_cast<int>(static_cast<long long>(kblocks) * (rank + 1) / kLoraCluster);
+  const int k0 = static_cast<int>(static_cast<long long>(kblocks) * rank / CL);
+  const int k1 = static_cast<int>(static_cast<long long>(kblocks) * (rank + 1) / CL);
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   const __nv_bfloat16* x0 = p.x + static_cast<size_t>(max(row0, 0)) * p.K + q * 8;
   const __nv_bfloat16* x1 = p.x + static_cast<size_t>(max(row1, 0)) * p.K + q * 8;
@@ -212,7 +211,7 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRows<NT>::CTAS) lora_rows_ke
   for (int i = threadIdx.x; i < 16 * RP / 4; i += kLoraThreads) {
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-    for (int c = 0; c < kLoraCluster; ++c) {
+    for (int c = 0; c < CL; ++c) {
       const float4 w = ld_dsmem_f4(mapa_shared(part + i * 16, c));
       v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
     }

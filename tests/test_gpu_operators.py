@@ -302,7 +302,7 @@ LORAS = [  # M, K, N, R, L
     (1, 16, 8, 8, 1), (1, 7168, 4096, 16, 4), (3, 48, 40, 24, 2), (17, 272, 264, 16, 1), (40, 528, 72, 32, 3),
     (64, 1040, 1032, 40, 64), (130, 256, 520, 64, 5), (33, 512, 136, 128, 2), (300, 144, 104, 96, 4),
     (700, 400, 200, 8, 3), (500, 272, 136, 128, 2), (1000, 1040, 264, 64, 5), (2100, 80, 72, 32, 300), (257, 16, 8, 48, 1),
-    (1500, 4112, 520, 40, 9),
+    (1500, 4112, 520, 40, 9), (600, 64, 40, 8, 1500), (256, 528, 264, 128, 30), (255, 144, 72, 72, 1),
 ]
 
 
