@@ -1,14 +1,18 @@
-"""Build the sm_100a CUDA library in-tree (nvcc, no JIT): libfp8gemm.so next to this file."""
+"""Build the sm_100a CUDA library in-tree (nvcc, no JIT), libfp8gemm.so, and the compiled part of the Python
+binding (g++), _operators.so, next to this file."""
 from __future__ import annotations
 
+import importlib.util
 import os
 import pathlib
 import subprocess
+import sysconfig
 
 HERE = pathlib.Path(__file__).resolve().parent
 ROOT = HERE.parent
 SO = HERE / "libfp8gemm.so"
 SO_DEBUG = HERE / "libfp8gemm_debug.so"  # the same library with the device-side checks (-DFG_DEBUG)
+BINDING = HERE / "_operators.so"  # marshalling of the operators (operators.py)
 CSRC = HERE / "csrc"
 COMMON = [CSRC / "fp8_cast_kernels.cuh", CSRC / "sm100_ptx.cuh", ROOT / "include" / "fp8gemm.h"]
 # source -> what it includes
@@ -84,12 +88,30 @@ def _build_one(so: pathlib.Path, extra, force: bool, verbose: bool) -> pathlib.P
     return so
 
 
+def build_binding(force: bool = False) -> pathlib.Path:
+    """Compile the marshalling of the operators against the installed torch, linked to libfp8gemm.so beside it."""
+    src = CSRC / "operators_binding.cpp"
+    if not force and _newer(BINDING, [src, ROOT / "include" / "fp8gemm.h", pathlib.Path(__file__)]):
+        return BINDING
+    torch = pathlib.Path(importlib.util.find_spec("torch").submodule_search_locations[0])
+    cuda = pathlib.Path(nvcc()).parent.parent if os.path.isabs(nvcc()) else pathlib.Path("/usr/local/cuda")
+    includes = [ROOT / "include", sysconfig.get_paths()["include"], torch / "include", cuda / "include"]
+    tmp = BINDING.with_suffix(".so.tmp%d" % os.getpid())
+    subprocess.check_call(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", *(f"-I{i}" for i in includes), str(src), "-o",
+                           str(tmp), f"-L{HERE}", "-l:libfp8gemm.so", "-Wl,-rpath,$ORIGIN", f"-L{torch / 'lib'}",
+                           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = True) -> pathlib.Path:
     """Compile the library (and, with debug=True, its debug build) if any source is newer than
     the built .so."""
     if debug:
         _build_one(SO_DEBUG, ["-DFG_DEBUG"], force, False)
-    return _build_one(SO, [], force, verbose)
+    so = _build_one(SO, [], force, verbose)
+    build_binding(force)
+    return so
 
 
 if __name__ == "__main__":

@@ -379,6 +379,66 @@ def test_lora_empty(fg):
     assert torch.equal(fg.lora_add(C, z(3, 16), z(2, 0, 16), z(2, 8, 0), ids), C)  # rank 0
 
 
+# ------------------------------------------------------------------------------------- refusals
+def test_binding_refuses(fg):
+    """Shapes, types, devices, streams and overlapping outputs, before anything is launched."""
+    b = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    f = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    logits = f(4, 8)
+    for bad in (0, 9):
+        with pytest.raises(ValueError, match="top_k"):
+            fg.moe_route(logits, bad)
+    with pytest.raises(fg.FP8GemmError, match="UNSUPPORTED"):
+        fg.moe_route(f(2, 64), 33)
+    with pytest.raises(fg.FP8GemmError, match="UNSUPPORTED"):
+        fg.moe_route(f(2, 1025), 2)
+    with pytest.raises(ValueError, match="contiguous"):
+        fg.moe_route(f(8, 4).t(), 2)
+    with pytest.raises(TypeError, match="mask"):
+        fg.moe_route(logits, 2, mask=torch.ones(4, device="cuda"))
+    with pytest.raises(TypeError, match="mask"):
+        fg.moe_route(logits, 2, mask=torch.ones(4, dtype=torch.bool))
+    with pytest.raises(ValueError, match="mask must have shape"):
+        fg.moe_route(logits, 2, mask=torch.ones(5, dtype=torch.bool, device="cuda"))
+    with pytest.raises(ValueError, match="slope"):
+        fg.moe_route_backward(logits, i(4, 2), f(7))
+    with pytest.raises(ValueError, match="ids"):
+        fg.moe_route_backward(logits, i(5, 2), f(8))
+    with pytest.raises(ValueError, match="num_experts"):
+        fg.moe_layout_contiguous(i(4, 2), 1025)
+    with pytest.raises(ValueError, match="num_experts"):
+        fg.moe_layout_masked(i(4, 2), 0, 4)
+    with pytest.raises(ValueError, match="rows"):
+        fg.moe_dispatch_fp8(b(4, 16), i(5, 2), shape=128)
+    with pytest.raises(ValueError, match="shape"):
+        fg.moe_dispatch_fp8(b(4, 16), i(4, 2))
+    with pytest.raises(fg.FP8GemmError, match="ALIGNMENT"):
+        fg.moe_dispatch_fp8(b(4, 24), i(4, 2), shape=128)
+    with pytest.raises(ValueError, match="sfa must have shape"):
+        fg.moe_dispatch_fp8(b(4, 16), i(4, 2), A=torch.zeros(128, 16, dtype=torch.uint8, device="cuda"), sfa=f(1, 127))
+    C = b(12, 16)
+    with pytest.raises(ValueError, match="out must not overlap C"):
+        fg.moe_combine(C, i(4, 2), out=C[8:])
+    with pytest.raises(ValueError, match="grad_C must not overlap C"):
+        fg.moe_combine_backward(b(4, 16), C, i(4, 2), f(4, 2), grad_C=C)
+    with pytest.raises(fg.FP8GemmError, match="UNSUPPORTED"):
+        fg.moe_combine(C, i(4, 33))
+    big = b(8, 16)
+    with pytest.raises(ValueError, match="out must not overlap C"):
+        fg.lora_add(big[:4], b(4, 16), b(1, 8, 16), b(1, 16, 8), i(4), out=big[2:6])
+    with pytest.raises(ValueError, match="out must not overlap x"):
+        fg.lora_add(C[:4], big[:4], b(1, 8, 16), b(1, 16, 8), i(4), out=big[:4])
+    with pytest.raises(ValueError, match="lora_b"):
+        fg.lora_add(C[:4], big[:4], b(1, 8, 16), b(1, 16, 16), i(4))
+    with pytest.raises(fg.FP8GemmError, match="UNSUPPORTED"):
+        fg.lora_add(C[:4], big[:4], b(1, 136, 16), b(1, 16, 136), i(4))
+    with pytest.raises(TypeError, match="tensor"):
+        fg.lora_add(C[:4], big[:4], b(1, 8, 16), b(1, 16, 8), [0, 0, 0, 0])
+    with pytest.raises(ValueError, match="stream"):
+        fg.moe_combine(torch.zeros(4, 16, dtype=torch.bfloat16), i(4, 2), stream=torch.cuda.Stream())
+
+
 # ------------------------------------------------------------------------------------- together
 def layer_inputs(T, E, K, H, N, seed):
     g = gen(seed)

@@ -128,11 +128,3 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         fg.lora_add(z(4, 16), z(4, 16), z(1, 8, 16), z(1, 16, 8), z(4, dtype=torch.int32))
     with pytest.raises(ValueError, match="mmax"):
         fg.moe_layout_masked(z(4, 2, dtype=torch.int32), 8, 0)
-
-
-def test_overlapping_outputs_are_found():
-    from moe_grouped_gemm_08_b200 import operators
-    buf = torch.zeros(100)
-    with pytest.raises(ValueError, match="out must not overlap C"):
-        operators._apart(buf[:60], "out", C=buf[50:])
-    operators._apart(buf[:50], "out", C=buf[50:], weights=None)
