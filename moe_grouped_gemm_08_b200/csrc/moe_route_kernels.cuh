@@ -105,9 +105,15 @@ __device__ __forceinline__ float row_sum(float x) {
 }
 template <int LPR>
 __device__ __forceinline__ float row_max(float v) {
+  if constexpr (LPR == 32) {  // one integer reduction of the bits made monotonic
+    const uint32_t u = __float_as_uint(v);
+    const uint32_t top = __reduce_max_sync(0xffffffffu, u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u));
+    return __uint_as_float((top & 0x80000000u) ? (top & 0x7FFFFFFFu) : ~top);
+  } else {
 #pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+    for (int o = LPR / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
 }
 template <int LPR>
 __device__ __forceinline__ uint32_t row_best(uint32_t v) {
@@ -282,6 +288,16 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
   for (; r0 < last; r0 += kRouteWarps * RPW) {
     const int r = r0 + rw;
     const bool live = r < last && next_live;
+    if (__ballot_sync(0xffffffffu, live) == 0) {  // all of the warp's rows are masked
+      if (r < last) {
+        for (int j = sub; j < p.k; j += LPR) {
+          ids[static_cast<size_t>(r) * p.k + j] = -1;
+          weights[static_cast<size_t>(r) * p.k + j] = 0.0f;
+        }
+      }
+      if (r0 + kRouteWarps * RPW < last) fetch(r0 + kRouteWarps * RPW);
+      continue;
+    }
     float x[NPL];
     K key[NPL];
 #pragma unroll
@@ -300,14 +316,28 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
       x[i] = softmax_exp(x[i], high);
       sum += x[i];
     }
-    for (int j = 0; j < p.k; ++j) {
-      if (key[0] == best) {  // the winner's lane (keys differ by their columns; 0 once a list is empty)
-        keys[j] = best;
+    // the winner's lane records the choice and moves its list on (keys differ by their columns; 0 once a list
+    // is empty).  Up to eight choices, the common case: only as much of a list is moved as is still needed.
+    if (p.k <= 8) {
 #pragma unroll
-        for (int i = 0; i + 1 < NPL; ++i) key[i] = key[i + 1];
-        key[NPL - 1] = 0;
+      for (int j = 0; j < 8; ++j) {
+        if (j >= p.k) break;
+        if (key[0] == best) {
+          keys[j] = best;
+#pragma unroll
+          for (int i = 0; i < (NPL < 7 - j ? NPL : 7 - j); ++i) key[i] = i + 1 < NPL ? key[i + 1] : K(0);
+        }
+        if (j + 1 < p.k) best = row_best<LPR>(key[0]);
       }
-      best = row_best<LPR>(key[0]);
+    } else {
+      for (int j = 0; j < p.k; ++j) {
+        if (key[0] == best) {
+          keys[j] = best;
+#pragma unroll
+          for (int i = 0; i < NPL; ++i) key[i] = i + 1 < NPL ? key[i + 1] : K(0);
+        }
+        best = row_best<LPR>(key[0]);
+      }
     }
     __syncwarp();
     float sums[2] = {sum, 0.0f};  // over all columns; over the choices
@@ -392,14 +422,17 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
   }
 }
 
-// Sums of the chunks of one sequence in a fixed order, then its counts, slopes and loss.  1024 threads:
-// as many parts of the chunks as columns leave room for, summed side by side.
+// Sums of the chunks of one sequence in a fixed order, then its counts, slopes and loss.  A cluster of
+// kFinishCluster CTAs of 1024 threads: each takes as many parts of the chunks side by side as columns leave room
+// for, and the first sums the CTAs' parts over distributed shared memory (592 chunks of 256 columns:
+// 4 us, 20 us with one CTA).
+constexpr int kFinishCluster = 8;
 __global__ void __launch_bounds__(1024) moe_route_finish_kernel(const RouteParams p) {
   __shared__ float s_part[1024];
   __shared__ int s_cnt[1024];
   __shared__ float s_red[32];
   __shared__ int s_total, s_rows;
-  const int seq = blockIdx.x;
+  const int seq = blockIdx.y, rank = static_cast<int>(cluster_ctarank());
   if (threadIdx.x == 0) s_rows = 0;
   __syncthreads();
   pdl_wait_prior_grid();
@@ -411,7 +444,7 @@ __global__ void __launch_bounds__(1024) moe_route_finish_kernel(const RouteParam
   int n = 0;
   if (e < p.E && part < parts) {
 #pragma unroll 8
-    for (int c = part; c < p.chunks; c += parts) {
+    for (int c = rank * parts + part; c < p.chunks; c += kFinishCluster * parts) {
       sum += p.part_p[(slot + c) * p.E + e];
       n += p.part_n[(slot + c) * (p.E + 1) + e];
     }
@@ -419,7 +452,8 @@ __global__ void __launch_bounds__(1024) moe_route_finish_kernel(const RouteParam
   s_part[threadIdx.x] = sum;
   s_cnt[threadIdx.x] = n;
   int rows = 0;
-  for (int c = threadIdx.x; c < p.chunks; c += 1024) rows += p.part_n[(slot + c) * (p.E + 1) + p.E];
+  for (int c = rank * 1024 + threadIdx.x; c < p.chunks; c += kFinishCluster * 1024)
+    rows += p.part_n[(slot + c) * (p.E + 1) + p.E];
   if (rows) atomicAdd(&s_rows, rows);
   __syncthreads();
   if (part == 0) {
@@ -427,9 +461,26 @@ __global__ void __launch_bounds__(1024) moe_route_finish_kernel(const RouteParam
       sum += s_part[q * cols + e];
       n += s_cnt[q * cols + e];
     }
+    s_part[e] = sum;
+    s_cnt[e] = n;
   }
+  cluster_sync_all();
+  if (rank == 0) {
+    sum = 0.0f;
+    n = 0;
+    rows = 0;
+    const uint32_t sum_at = smem_addr(&s_part[e]), n_at = smem_addr(&s_cnt[e]), rows_at = smem_addr(&s_rows);
+#pragma unroll
+    for (int c = 0; c < kFinishCluster; ++c) {
+      sum += ld_dsmem_f32(mapa_shared(sum_at, c));
+      n += __float_as_int(ld_dsmem_f32(mapa_shared(n_at, c)));
+      rows += __float_as_int(ld_dsmem_f32(mapa_shared(rows_at, c)));
+    }
+  }
+  cluster_sync_all();  // the parts have been read
+  if (rank != 0) return;
   // columns past E (and threads of other parts) hold nothing
-  route_finish(p, seq, sum, threadIdx.x < p.E ? n : 0, s_rows, s_red, &s_total);
+  route_finish(p, seq, sum, threadIdx.x < p.E ? n : 0, rows, s_red, &s_total);
 }
 
 struct RouteGradParams {
@@ -503,6 +554,26 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_backward_kernel(const
     const int id = next_id;
     const float gw = next_g;
     if (r0 + kRouteWarps * RPW < last) fetch(r0 + kRouteWarps * RPW);
+    bool any = id >= 0;
+    if constexpr (LPR < kRouteMaxK) {
+      for (int j = sub + LPR; j < p.k; j += LPR) any |= static_cast<unsigned>(ids[static_cast<size_t>(r) * p.k + j]) < static_cast<unsigned>(p.E);
+    }
+    const uint32_t votes = __ballot_sync(0xffffffffu, any);
+    const bool routed = (votes >> (rw * LPR)) & (LPR == 32 ? 0xffffffffu : (1u << (LPR & 31)) - 1);
+    T* out = out_all + static_cast<size_t>(r) * p.E;
+    const bool write = r0 + rw < last;
+    if (votes == 0) {  // none of the warp's rows was routed
+#pragma unroll
+      for (int i = 0; i < NPL; i += V) {
+        const int c = route_col<LPR, V>(i, sub);
+        if (c >= p.E || !write) continue;
+        if constexpr (V == 1)
+          out[c] = from_f32<T>(0.0f);
+        else
+          *reinterpret_cast<uint4*>(out + c) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      continue;
+    }
     const float chosen = id >= 0 ? to_f32(logits[id]) : 0.0f;  // the row's own: in L1
     const float high = row_max<LPR>(m);
     // sums of u, of u h, of u over the choices, of u g over the choices
@@ -513,7 +584,6 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_backward_kernel(const
       sums[0] += x[i];
       sums[1] = fmaf(x[i], h[i], sums[1]);
     }
-    bool any = id >= 0;
     const float u = id >= 0 ? softmax_exp(chosen, high) : 0.0f;
     sums[2] = u;
     sums[3] = id >= 0 ? u * gw : 0.0f;
@@ -523,14 +593,11 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_backward_kernel(const
         float gw2;
         choice(r, j, id2, gw2);
         if (id2 < 0) continue;
-        any = true;
         const float u2 = softmax_exp(to_f32(logits[id2]), high);
         sums[2] += u2;
         sums[3] = fmaf(u2, gw2, sums[3]);
       }
     }
-    const uint32_t votes = __ballot_sync(0xffffffffu, any);
-    const bool routed = (votes >> (rw * LPR)) & (LPR == 32 ? 0xffffffffu : (1u << (LPR & 31)) - 1);
     row_sums<LPR>(sums);
     const float inv = 1.0f / sums[0];
     const float top = p.renorm ? 1.0f / sums[2] : inv;
@@ -548,8 +615,6 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_backward_kernel(const
       }
       __syncwarp();
     }
-    T* out = out_all + static_cast<size_t>(r) * p.E;
-    const bool write = r0 + rw < last;
 #pragma unroll
     for (int i = 0; i < NPL; i += V) {
       const int c = route_col<LPR, V>(i, sub);

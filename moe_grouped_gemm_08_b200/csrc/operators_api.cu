@@ -374,7 +374,7 @@ fg_status fg_moe_route(const void* logits, int dtype, const unsigned char* mask,
     const fg_status s = route_dispatch(p, S, dtype, r.cluster, wide, stream);
     if (s != FG_OK || r.cluster) return s;
   }
-  return launch(fg::moe_route_finish_kernel, dim3(S), 1024, 0, stream, 1, p);
+  return launch(fg::moe_route_finish_kernel, dim3(fg::kFinishCluster, S), 1024, 0, stream, fg::kFinishCluster, p);
 }
 
 fg_status fg_moe_route_backward(const void* logits, int dtype, const int* ids, const float* slope,
