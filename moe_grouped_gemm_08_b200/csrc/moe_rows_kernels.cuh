@@ -395,75 +395,73 @@ __device__ __forceinline__ float warp_sum8(float (&v)[8], int lane) {
 }
 
 // grad_C[rows[t][j]] = weights[t][j] grad_out[t];  grad_weights[t][j] = <grad_out[t], C[rows[t][j]]>.
-// One CTA per token, 16 columns per thread and pass; eight choices at a time, their dot products in
-// registers, the rows of four asked for before the first is used.
-constexpr int kCombineGradThreads = 128;
-__global__ void __launch_bounds__(kCombineGradThreads) moe_combine_backward_kernel(const CombineGradParams p) {
+// One CTA per token and eight choices, 8 columns per thread and pass: all eight rows are asked for before the
+// first is used, and the next token's rows and weights are loaded meanwhile; dot products in registers.
+constexpr int kCombineGradThreads = 256;
+__global__ void __launch_bounds__(kCombineGradThreads, 3) moe_combine_backward_kernel(const CombineGradParams p) {
   constexpr int W = kCombineGradThreads / 32, SPAN = kCombineGradThreads * 8;
   __shared__ float s_dot[2][W][8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int buf = 0;
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  for (long long t = blockIdx.x; t < p.T; t += gridDim.x) {
-    for (int j0 = 0; j0 < p.k; j0 += 8) {
-      const int j_here = j0 + (lane & 7);
-      int mine = j_here < p.k ? p.rows[t * p.k + j_here] : -1;
-      if (mine >= p.M) mine = -1;
-      const float mw = mine >= 0 ? p.weights[t * p.k + j_here] : 0.0f;
-      float dot[8] = {};
-      for (int col = threadIdx.x * 8; col - static_cast<int>(threadIdx.x) * 8 < p.N; col += 2 * SPAN) {
-        const bool first = col < p.N, second = col + SPAN < p.N;
-        const uint4* gsrc = reinterpret_cast<const uint4*>(p.grad_out + t * p.N + col);
-        uint4 graw[2];
-        graw[0] = first ? __ldg(gsrc) : make_uint4(0u, 0u, 0u, 0u);
-        graw[1] = second ? __ldg(gsrc + SPAN / 8) : make_uint4(0u, 0u, 0u, 0u);
+  const int groups = (p.k + 7) / 8;
+  const long long items = p.T * groups;  // a token and eight of its choices
+  int row_next = -1;
+  float w_next = 0.0f;
+  auto fetch = [&](long long item) {
+    const long long t = groups == 1 ? item : item / groups;
+    const int j = static_cast<int>(item - t * groups) * 8 + (lane & 7);
+    row_next = j < p.k ? p.rows[t * p.k + j] : -1;
+    if (row_next >= p.M) row_next = -1;
+    w_next = j < p.k ? p.weights[t * p.k + j] : 0.0f;
+  };
+  if (blockIdx.x < items) fetch(blockIdx.x);
+  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+    const long long t = groups == 1 ? item : item / groups;
+    const int j0 = static_cast<int>(item - t * groups) * 8;
+    const int mine = row_next;
+    const float mw = w_next;
+    float dot[8] = {};
+    for (int c0 = 0; c0 < p.N; c0 += SPAN) {
+      const int col = c0 + threadIdx.x * 8;
+      const bool in = col < p.N;
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      const uint4 graw = in ? __ldg(reinterpret_cast<const uint4*>(p.grad_out + t * p.N + col)) : zero;
+      uint4 raw[8];
 #pragma unroll
-        for (int jb = 0; jb < 8; jb += 4) {
-          if (j0 + jb >= p.k) break;
-          uint4 raw[4][2];
-          int row[4];
+      for (int j = 0; j < 8; ++j) {
+        const int row = __shfl_sync(0xffffffffu, mine, j);
+        raw[j] = row >= 0 && in ? __ldg(reinterpret_cast<const uint4*>(p.C + static_cast<size_t>(row) * p.N + col)) : zero;
+      }
+      if (c0 == 0 && item + gridDim.x < items) fetch(item + gridDim.x);
+      float g[8];
+      unpack_bf16x8(graw, g);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            row[j] = __shfl_sync(0xffffffffu, mine, jb + j);
-            const uint4* src = reinterpret_cast<const uint4*>(p.C + static_cast<size_t>(max(row[j], 0)) * p.N + col);
-            raw[j][0] = row[j] >= 0 && first ? __ldg(src) : make_uint4(0u, 0u, 0u, 0u);
-            raw[j][1] = row[j] >= 0 && second ? __ldg(src + SPAN / 8) : make_uint4(0u, 0u, 0u, 0u);
-          }
-          float g[2][8];
-          unpack_bf16x8(graw[0], g[0]);
-          unpack_bf16x8(graw[1], g[1]);
+      for (int j = 0; j < 8; ++j) {
+        const int row = __shfl_sync(0xffffffffu, mine, j);
+        const float w = __shfl_sync(0xffffffffu, mw, j);
+        float f[8], o[8];
+        unpack_bf16x8(raw[j], f);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float w = __shfl_sync(0xffffffffu, mw, jb + j);
-            if (row[j] < 0) continue;
-            uint4* dst = reinterpret_cast<uint4*>(p.grad_C + static_cast<size_t>(row[j]) * p.N + col);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float f[8], o[8];
-              unpack_bf16x8(raw[j][h], f);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                dot[jb + j] = fmaf(g[h][i], f[i], dot[jb + j]);
-                o[i] = w * g[h][i];
-              }
-              if (h == 0 ? first : second) dst[h * (SPAN / 8)] = pack_bf16x8(o);
-            }
-          }
+        for (int i = 0; i < 8; ++i) {
+          dot[j] = fmaf(g[i], f[i], dot[j]);
+          o[i] = w * g[i];
         }
+        if (row >= 0 && in) *reinterpret_cast<uint4*>(p.grad_C + static_cast<size_t>(row) * p.N + col) = pack_bf16x8(o);
       }
-      __syncwarp();
-      const float v = warp_sum8(dot, lane);
-      if ((lane & 3) == 0) s_dot[buf][warp][lane >> 2] = v;
-      __syncthreads();
-      if (threadIdx.x < 8 && j0 + static_cast<int>(threadIdx.x) < p.k) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < W; ++i) sum += s_dot[buf][i][threadIdx.x];
-        p.grad_weights[t * p.k + j0 + threadIdx.x] = sum;
-      }
-      buf ^= 1;  // the other buffer's readers are past the barrier above
     }
+    if (p.N == 0 && item + gridDim.x < items) fetch(item + gridDim.x);
+    const float v = warp_sum8(dot, lane);
+    if ((lane & 3) == 0) s_dot[buf][warp][lane >> 2] = v;
+    __syncthreads();
+    if (threadIdx.x < 8 && j0 + static_cast<int>(threadIdx.x) < p.k) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) sum += s_dot[buf][i][threadIdx.x];
+      p.grad_weights[t * p.k + j0 + threadIdx.x] = sum;
+    }
+    buf ^= 1;  // the other buffer's readers are past the barrier above
   }
 }
 
