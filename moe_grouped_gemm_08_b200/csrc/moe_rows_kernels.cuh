@@ -395,23 +395,25 @@ __device__ __forceinline__ float warp_sum8(float (&v)[8], int lane) {
 }
 
 // grad_C[rows[t][j]] = weights[t][j] grad_out[t];  grad_weights[t][j] = <grad_out[t], C[rows[t][j]]>.
-// One CTA per token and eight choices, 8 columns per thread and pass: all eight rows are asked for before the
-// first is used, and the next token's rows and weights are loaded meanwhile; dot products in registers.
+// One CTA per token and J choices, V vectors of 8 columns per thread and pass, J V = 8: all eight vectors of C
+// are asked for before the first is used, and the next token's rows and weights are loaded meanwhile;
+// dot products in registers.
 constexpr int kCombineGradThreads = 256;
+template <int J>
 __global__ void __launch_bounds__(kCombineGradThreads, 3) moe_combine_backward_kernel(const CombineGradParams p) {
-  constexpr int W = kCombineGradThreads / 32, SPAN = kCombineGradThreads * 8;
+  constexpr int W = kCombineGradThreads / 32, V = 8 / J, SPAN = kCombineGradThreads * 8;
   __shared__ float s_dot[2][W][8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int buf = 0;
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  const int groups = (p.k + 7) / 8;
-  const long long items = p.T * groups;  // a token and eight of its choices
+  const int groups = (p.k + J - 1) / J;
+  const long long items = p.T * groups;  // a token and J of its choices
   int row_next = -1;
   float w_next = 0.0f;
   auto fetch = [&](long long item) {
     const long long t = groups == 1 ? item : item / groups;
-    const int j = static_cast<int>(item - t * groups) * 8 + (lane & 7);
+    const int j = static_cast<int>(item - t * groups) * J + lane % J;
     row_next = j < p.k ? p.rows[t * p.k + j] : -1;
     if (row_next >= p.M) row_next = -1;
     w_next = j < p.k ? p.weights[t * p.k + j] : 0.0f;
@@ -419,43 +421,51 @@ __global__ void __launch_bounds__(kCombineGradThreads, 3) moe_combine_backward_k
   if (blockIdx.x < items) fetch(blockIdx.x);
   for (long long item = blockIdx.x; item < items; item += gridDim.x) {
     const long long t = groups == 1 ? item : item / groups;
-    const int j0 = static_cast<int>(item - t * groups) * 8;
+    const int j0 = static_cast<int>(item - t * groups) * J;
     const int mine = row_next;
     const float mw = w_next;
+    if (item + gridDim.x < items) fetch(item + gridDim.x);
     float dot[8] = {};
-    for (int c0 = 0; c0 < p.N; c0 += SPAN) {
-      const int col = c0 + threadIdx.x * 8;
-      const bool in = col < p.N;
+    for (int c0 = 0; c0 < p.N; c0 += V * SPAN) {
+      const int col0 = c0 + threadIdx.x * 8;
       const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-      const uint4 graw = in ? __ldg(reinterpret_cast<const uint4*>(p.grad_out + t * p.N + col)) : zero;
-      uint4 raw[8];
+      uint4 graw[V], raw[V][J];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int row = __shfl_sync(0xffffffffu, mine, j);
-        raw[j] = row >= 0 && in ? __ldg(reinterpret_cast<const uint4*>(p.C + static_cast<size_t>(row) * p.N + col)) : zero;
-      }
-      if (c0 == 0 && item + gridDim.x < items) fetch(item + gridDim.x);
-      float g[8];
-      unpack_bf16x8(graw, g);
+      for (int v = 0; v < V; ++v) {
+        const int col = col0 + v * SPAN;
+        graw[v] = col < p.N ? __ldg(reinterpret_cast<const uint4*>(p.grad_out + t * p.N + col)) : zero;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int row = __shfl_sync(0xffffffffu, mine, j);
-        const float w = __shfl_sync(0xffffffffu, mw, j);
-        float f[8], o[8];
-        unpack_bf16x8(raw[j], f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          dot[j] = fmaf(g[i], f[i], dot[j]);
-          o[i] = w * g[i];
+        for (int j = 0; j < J; ++j) {
+          const int row = __shfl_sync(0xffffffffu, mine, j);
+          raw[v][j] = row >= 0 && col < p.N
+                          ? __ldg(reinterpret_cast<const uint4*>(p.C + static_cast<size_t>(row) * p.N + col)) : zero;
         }
-        if (row >= 0 && in) *reinterpret_cast<uint4*>(p.grad_C + static_cast<size_t>(row) * p.N + col) = pack_bf16x8(o);
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int col = col0 + v * SPAN;
+        float g[8];
+        unpack_bf16x8(graw[v], g);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const int row = __shfl_sync(0xffffffffu, mine, j);
+          const float w = __shfl_sync(0xffffffffu, mw, j);
+          float f[8], o[8];
+          unpack_bf16x8(raw[v][j], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            dot[j] = fmaf(g[i], f[i], dot[j]);
+            o[i] = w * g[i];
+          }
+          if (row >= 0 && col < p.N)
+            *reinterpret_cast<uint4*>(p.grad_C + static_cast<size_t>(row) * p.N + col) = pack_bf16x8(o);
+        }
       }
     }
-    if (p.N == 0 && item + gridDim.x < items) fetch(item + gridDim.x);
-    const float v = warp_sum8(dot, lane);
-    if ((lane & 3) == 0) s_dot[buf][warp][lane >> 2] = v;
+    const float sum8 = warp_sum8(dot, lane);
+    if ((lane & 3) == 0) s_dot[buf][warp][lane >> 2] = sum8;
     __syncthreads();
-    if (threadIdx.x < 8 && j0 + static_cast<int>(threadIdx.x) < p.k) {
+    if (threadIdx.x < J && j0 + static_cast<int>(threadIdx.x) < p.k) {
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < W; ++i) sum += s_dot[buf][i][threadIdx.x];

@@ -513,8 +513,10 @@ fg_status fg_moe_combine_backward(const void* grad_out, const void* C, const int
   p.k = k;
   p.N = N;
   p.M = M;
-  return launch_walk<fg::moe_combine_backward_kernel>(static_cast<long long>(T) * ((k + 7) / 8), fg::kCombineGradThreads,
-                                                     stream, p);
+  const long long tokens = T;
+  if (k <= 2) return launch_walk<fg::moe_combine_backward_kernel<2>>(tokens, fg::kCombineGradThreads, stream, p);
+  if (k <= 4) return launch_walk<fg::moe_combine_backward_kernel<4>>(tokens, fg::kCombineGradThreads, stream, p);
+  return launch_walk<fg::moe_combine_backward_kernel<8>>(tokens * cdiv(k, 8), fg::kCombineGradThreads, stream, p);
 }
 
 size_t fg_lora_scratch_bytes(int M, int R, int L) {
