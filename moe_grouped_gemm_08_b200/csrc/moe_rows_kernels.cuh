@@ -308,59 +308,67 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&f)[8]) {
   return *reinterpret_cast<const uint4*>(h);
 }
 
-// out[t] = sum_j weights[t][j] C[rows[t][j]] in fp32, rounded once.  One warp per token and 256 columns,
-// 8 per lane.  B = 4: four rows are asked for before the first is used (8 choices of 2048 columns: 27
-// us for 151 MB, 32 us with B = 1); with one or two choices B = 1, whose 32 registers let an SM hold 64 warps
-// (2 choices of 7168 columns: 121 us for 705 MB, 137 us with B = 2).
-template <int B>
-__global__ void __launch_bounds__(256, B == 1 ? 8 : 5) moe_combine_kernel(const CombineParams p, int chunks) {
+// out[t] = sum_j weights[t][j] C[rows[t][j]] in fp32, rounded once, in the order of j.  One warp per token and V
+// vectors of 8 columns per lane, J choices at a time, J V = 8: all eight vectors are asked for before the first is
+// used, and the next token's rows and weights are loaded meanwhile.  Bound by HBM: 705 MB in 105 us (2 choices of
+// 7168 columns, J = 2; 124 us with one vector a lane and 64 warps an SM), 151 MB in 26 us (8 choices of
+// 2048, J = 4; 29 us with J = 8).
+template <int J>
+__global__ void __launch_bounds__(256, 3) moe_combine_kernel(const CombineParams p, int chunks) {
+  constexpr int V = 8 / J;
   const int lane = threadIdx.x & 31;
   const long long nwarps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
+  const long long items = p.T * chunks;
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  for (long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; w < p.T * chunks;
-       w += nwarps) {
+  long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  int row_next = -1;
+  float w_next = 0.0f;
+  auto fetch = [&](long long item) {
+    const long long t = item / chunks;
+    row_next = lane < p.k ? p.rows[t * p.k + lane] : -1;
+    if (row_next >= p.M) row_next = -1;
+    w_next = !p.weights ? 1.0f : lane < p.k ? p.weights[t * p.k + lane] : 0.0f;
+  };
+  if (w < items) fetch(w);
+  for (; w < items; w += nwarps) {
     const long long t = w / chunks;
-    const int col = static_cast<int>(w - t * chunks) * 256 + lane * 8;
-    const bool in = col < p.N;
-    int mine = lane < p.k ? p.rows[t * p.k + lane] : -1;
-    if (mine >= p.M) mine = -1;
-    const float mw = mine >= 0 ? (p.weights ? p.weights[t * p.k + lane] : 1.0f) : 0.0f;
-    float acc[8] = {};
-    if constexpr (B == 1) {
-      for (int q = 0; q < p.k; ++q) {
-        const int row = __shfl_sync(0xffffffffu, mine, q);
-        const float wq = __shfl_sync(0xffffffffu, mw, q);
-        if (row < 0 || !in) continue;
-        float f[8];
-        unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(p.C + static_cast<size_t>(row) * p.N + col)), f);
+    const int col0 = static_cast<int>(w - t * chunks) * (V * 256) + lane * 8;
+    const int mine = row_next;
+    const float mw = w_next;
+    if (w + nwarps < items) fetch(w + nwarps);
+    float acc[V][8] = {};
+    for (int q0 = 0; q0 < p.k; q0 += J) {
+      uint4 raw[J][V];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = fmaf(wq, f[i], acc[i]);
-      }
-    } else {
-      for (int q0 = 0; q0 < p.k; q0 += B) {
-        uint4 raw[B];
-        float wq[B];
-        bool has[B];
+      for (int q = 0; q < J; ++q) {
+        const int row = q0 + q < p.k ? __shfl_sync(0xffffffffu, mine, q0 + q) : -1;
 #pragma unroll
-        for (int q = 0; q < B; ++q) {
-          const int row = __shfl_sync(0xffffffffu, mine, (q0 + q) & 31);
-          wq[q] = __shfl_sync(0xffffffffu, mw, (q0 + q) & 31);
-          has[q] = q0 + q < p.k && row >= 0;
-          raw[q] = has[q] && in ? __ldg(reinterpret_cast<const uint4*>(p.C + static_cast<size_t>(row) * p.N + col))
-                                : make_uint4(0u, 0u, 0u, 0u);
+        for (int v = 0; v < V; ++v) {
+          const int col = col0 + v * 256;
+          raw[q][v] = row >= 0 && col < p.N
+                          ? __ldg(reinterpret_cast<const uint4*>(p.C + static_cast<size_t>(row) * p.N + col))
+                          : make_uint4(0u, 0u, 0u, 0u);
         }
+      }
 #pragma unroll
-        for (int q = 0; q < B; ++q) {
-          if (!has[q]) continue;
+      for (int q = 0; q < J; ++q) {
+        if (q0 + q >= p.k) break;
+        const int row = __shfl_sync(0xffffffffu, mine, q0 + q);
+        const float wq = __shfl_sync(0xffffffffu, mw, q0 + q);
+        if (row < 0) continue;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
           float f[8];
-          unpack_bf16x8(raw[q], f);
+          unpack_bf16x8(raw[q][v], f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i] = fmaf(wq[q], f[i], acc[i]);
+          for (int i = 0; i < 8; ++i) acc[v][i] = fmaf(wq, f[i], acc[v][i]);
         }
       }
     }
-    if (in) *reinterpret_cast<uint4*>(p.out + t * p.N + col) = pack_bf16x8(acc);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (col0 + v * 256 < p.N) *reinterpret_cast<uint4*>(p.out + t * p.N + col0 + v * 256) = pack_bf16x8(acc[v]);
   }
 }
 
@@ -397,7 +405,8 @@ __device__ __forceinline__ float warp_sum8(float (&v)[8], int lane) {
 // grad_C[rows[t][j]] = weights[t][j] grad_out[t];  grad_weights[t][j] = <grad_out[t], C[rows[t][j]]>.
 // One CTA per token and J choices, V vectors of 8 columns per thread and pass, J V = 8: all eight vectors of C
 // are asked for before the first is used, and the next token's rows and weights are loaded meanwhile;
-// dot products in registers.
+// dot products in registers.  Bound by HBM: 285 MB in 48 us (8 choices of 2048 columns), 1.17 GB in 192 us (2 of
+// 7168).
 constexpr int kCombineGradThreads = 256;
 template <int J>
 __global__ void __launch_bounds__(kCombineGradThreads, 3) moe_combine_backward_kernel(const CombineGradParams p) {

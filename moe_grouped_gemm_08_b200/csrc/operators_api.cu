@@ -7,6 +7,7 @@
 #include <atomic>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "fp8gemm.h"
 #include "lora_kernels.cuh"
@@ -486,10 +487,13 @@ fg_status fg_moe_combine(const void* C, const int* rows, const float* weights, v
   p.k = k;
   p.N = N;
   p.M = M;
-  const int chunks = static_cast<int>(cdiv(N, 256));
-  const long long blocks = cdiv(static_cast<long long>(T) * chunks, 8);
-  return k <= 2 ? launch_walk<fg::moe_combine_kernel<1>>(blocks, 256, stream, p, chunks)
-                : launch_walk<fg::moe_combine_kernel<4>>(blocks, 256, stream, p, chunks);
+  auto run = [&](auto choices) {  // so many choices at once
+    constexpr int J = decltype(choices)::value;
+    const int chunks = static_cast<int>(cdiv(N, 8 / J * 256));
+    return launch_walk<fg::moe_combine_kernel<J>>(cdiv(static_cast<long long>(T) * chunks, 8), 256, stream, p, chunks);
+  };
+  if (k <= 2) return run(std::integral_constant<int, 2>());
+  return run(std::integral_constant<int, 4>());
 }
 
 fg_status fg_moe_combine_backward(const void* grad_out, const void* C, const int* rows, const float* weights,
