@@ -232,7 +232,8 @@ fg_status fp8_cast_blocks_ex(const void* X, void* Q, float* sfb, int G, int N, i
 /* ------------------------------------------------------------------ around the GEMMs
  * The operators between a layer's tokens and the grouped GEMMs, and low-rank adapters beside
  * a projection.  All pointers are device pointers owned by the caller; nothing is allocated, no
- * call needs fg_init, and every call can be captured into a CUDA graph.  `scratch` is device
+ * call needs fg_init, and every call can be captured into a CUDA graph (make an operator's first
+ * call on a device outside of a capture: its kernels are loaded then).  `scratch` is device
  * memory of at least the stated size with any contents, needed until the call's kernels have
  * run; calls that may run at the same time need different scratch.  Results are deterministic.
  * Value types of the router's logits: */
@@ -310,8 +311,9 @@ fg_status fg_moe_combine_backward(const void* grad_out, const void* C, const int
  * x bf16 [M][K], lora_a bf16 [L][R][K], lora_b bf16 [L][N][R], scaling fp32 [L] or NULL (all 1).
  * Both products accumulate in fp32, A_a x is kept to 16 bits of mantissa between them, and the sum
  * is rounded once.  K % 16 == 0, N % 8 == 0, R % 8 == 0, R <= 128 (a smaller rank is padded with
- * zeros), M <= 2^24.  Rows of one adapter may stand anywhere; many rows are first sorted by adapter, which
- * takes the scratch (16-byte aligned).  The first call on a device is made outside stream capture.
+ * zeros), M <= 2^24, and M <= 2^18 with L >= FG_MOE_MAX_EXPERTS, else FG_ERR_UNSUPPORTED.  Rows of
+ * one adapter may stand anywhere; many rows are first sorted by adapter, which takes the scratch
+ * (16-byte aligned).  out overlaps C in whole or not at all, and no other operand.
  * A wait of a kernel for many rows that runs out (about two seconds) makes it write NaN and leave
  * FG_ERR_TIMEOUT for fg_lora_status, which synchronises `stream`, reads and clears it. */
 size_t fg_lora_scratch_bytes(int M, int R, int L);

@@ -339,12 +339,13 @@ __device__ __forceinline__ int lora_down_ctas(long long U, unsigned grid) {
   return static_cast<int>(most < grid ? most : grid);
 }
 
-// Rows of a tile that thread `tid` copies 16 bytes of: row_of + 32 i; -1 for padding.
+// Rows of a tile that thread `tid` copies 16 bytes of: row_of + 32 i; -1 for padding.  (The places are read past
+// L1: lora_up_kernel reads them before it has waited for lora_down_kernel.)
 __device__ __forceinline__ void lora_tile_rows(const LoraParams& p, int tile, int row_of, int (&row)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int at = tile * kLoraTileRows + row_of + 32 * i;
-    row[i] = p.group[at] >= 0 ? p.place_row[at] : -1;
+    row[i] = __ldcg(p.group + at) >= 0 ? __ldcg(p.place_row + at) : -1;
   }
 }
 
@@ -535,9 +536,9 @@ __global__ void __launch_bounds__(kLoraThreads, LoraTile<RP>::CTAS) lora_up_kern
   // parts of h, and what is written, come after the wait below.
   const int chunks = (p.N + 63) / 64;
   const int KB = (p.K + 63) / 64;
-  const long long U = static_cast<long long>(p.tiles[0]) * KB;
+  const long long U = static_cast<long long>(__ldcg(p.tiles)) * KB;
   const int PU = lora_down_ctas(U, gridDim.x);  // the grid of lora_down_kernel, as large as this one
-  const long long V = static_cast<long long>(p.tiles[0]) * chunks;
+  const long long V = static_cast<long long>(__ldcg(p.tiles)) * chunks;
   const int P = static_cast<int>(V < gridDim.x ? V : gridDim.x);
   int v = 0, v_end = 0;
   if (static_cast<int>(blockIdx.x) < P) {
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(kLoraThreads, LoraTile<RP>::CTAS) lora_up_kern
   while (v < v_end) {
     const int t = v / chunks, c0 = v - t * chunks;
     const int nc = min(chunks - c0, v_end - v);
-    const int ad = p.group[t * kLoraTileRows];
+    const int ad = __ldcg(p.group + t * kLoraTileRows);
     lora_tile_rows(p, t, row_of, row);
     const __nv_bfloat16* wb = p.b + static_cast<size_t>(ad) * p.N * p.R;
     auto load = [&](int c) {

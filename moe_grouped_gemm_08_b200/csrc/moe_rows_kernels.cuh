@@ -459,6 +459,7 @@ __global__ void __launch_bounds__(kCombineGradThreads, 3) moe_combine_backward_k
         for (int j = 0; j < J; ++j) {
           const int row = __shfl_sync(0xffffffffu, mine, j);
           const float w = __shfl_sync(0xffffffffu, mw, j);
+          if (row < 0) continue;  // its gradient stays 0, whatever grad_out holds
           float f[8], o[8];
           unpack_bf16x8(raw[v][j], f);
 #pragma unroll
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(kCombineGradThreads, 3) moe_combine_backward_k
             dot[j] = fmaf(g[i], f[i], dot[j]);
             o[i] = w * g[i];
           }
-          if (row >= 0 && col < p.N)
+          if (col < p.N)
             *reinterpret_cast<uint4*>(p.grad_C + static_cast<size_t>(row) * p.N + col) = pack_bf16x8(o);
         }
       }

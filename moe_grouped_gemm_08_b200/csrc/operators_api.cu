@@ -285,8 +285,11 @@ fg_status lora_tiles_launch(const fg::LoraParams& p, int sms, void* stream) {
   return launch(fg::lora_up_kernel<RP>, grid, fg::kLoraThreads, L::UP_SMEM, stream, 1, p);
 }
 
-// Many rows per adapter: tiles of 128 rows.  Few: groups of 16, found by the kernel itself.
+// Many rows: tiles of 128 rows, sorted by adapter (300 rows of 4 adapters, rank 64: 22 us either way).  Few, or more
+// adapters than the sort takes: groups of 16, which the kernel finds by reading all rows' adapters, so that
+// its time grows with the square of the rows (hence kMostUnsortedRows).
 bool lora_by_tiles(int M, int L) { return L > 0 && L < FG_MOE_MAX_EXPERTS && M > 256; }
+constexpr int kMostUnsortedRows = 1 << 18;
 
 // Scratch of the tiles: parts of h, then the places of the sorted rows (of the L adapters and of those without).
 struct LoraScratch {
@@ -542,6 +545,15 @@ fg_status fg_lora_add(const void* C, const void* x, const void* lora_a, const vo
   if (!aligned(C, 16) || !aligned(x, 16) || !aligned(lora_a, 16) || !aligned(lora_b, 16) || !aligned(out, 16) ||
       !aligned(adapters, 4) || !aligned(scaling, 4) || !aligned(scratch, 16))
     return FG_ERR_ALIGNMENT;
+  if (L >= FG_MOE_MAX_EXPERTS && M > kMostUnsortedRows) return FG_ERR_UNSUPPORTED;
+  if (L == 0) {
+    if (out != C && cudaMemcpyAsync(out, C, static_cast<size_t>(M) * N * 2, cudaMemcpyDeviceToDevice,
+                                    static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+      cudaGetLastError();
+      return FG_ERR_CUDA;
+    }
+    return FG_OK;
+  }
   fg::LoraParams p;
   std::memset(&p, 0, sizeof(p));
   p.C = static_cast<const __nv_bfloat16*>(C);

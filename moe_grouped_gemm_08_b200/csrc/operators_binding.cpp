@@ -128,6 +128,12 @@ int arg_int(PyObject* o, const char* what) {
   return static_cast<int>(v);
 }
 
+bool arg_bool(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised();
+  return v != 0;
+}
+
 PyObject* wrap(const Tensor& t) { return THPVariable_Wrap(t); }
 PyObject* given(PyObject* o) {
   Py_INCREF(o);
@@ -181,7 +187,7 @@ c10::SmallVector<int64_t, 4> joined(at::IntArrayRef lead, std::initializer_list<
 // (logits, k, mask, renormalize)
 PyObject* moe_route(PyObject* const* a) {
   const Logits l = logits_of(a[0]);
-  const int k = arg_int(a[1], "top_k"), renorm = PyObject_IsTrue(a[3]);
+  const int k = arg_int(a[1], "top_k"), renorm = arg_bool(a[3]);
   if (k < 1 || k > l.E)
     raise(PyExc_ValueError, "top_k must be in 1.." + std::to_string(l.E) + ", got " + std::to_string(k));
   const Tensor* mask = beside_or_none(a[2], at::kBool, joined(l.lead, {l.T}), l.t, "mask");
@@ -211,11 +217,11 @@ PyObject* moe_route_backward(PyObject* const* a) {
   const Tensor& slope = beside(a[2], at::kFloat, joined(l.lead, {l.E}), l.t, "slope");
   const Tensor* grad_weights = beside_or_none(a[3], at::kFloat, choices, l.t, "grad_weights");
   const Tensor* grad_loss = beside_or_none(a[4], at::kFloat, l.lead, l.t, "grad_loss");
+  const int renorm = arg_bool(a[5]);
   if (elsewhere(l.t)) Py_RETURN_NONE;
   const Tensor grad = empty(l.t.sizes(), l.t, l.t.scalar_type());
   check(fg_moe_route_backward(ptr(l.t), l.type, ptr<int>(ids), ptr<float>(slope), ptr<float>(grad_weights),
-                              ptr<float>(grad_loss), ptr(grad), l.S, l.T, l.E, k, PyObject_IsTrue(a[5]),
-                              stream_of(l.t)),
+                              ptr<float>(grad_loss), ptr(grad), l.S, l.T, l.E, k, renorm, stream_of(l.t)),
         "fg_moe_route_backward");
   return wrap(grad);
 }

@@ -286,6 +286,18 @@ def test_combine_and_its_gradients(fg, T, k, E, N, mmax):
     assert np.all(np.abs(f64(grad_w) - want_w) <= (N / 8 + 40) * U * size_w)
 
 
+def test_combine_gradient_of_pairs_without_a_row_is_zero(fg):
+    """... whatever the gradient of the sum and the weights hold."""
+    rows = torch.tensor([[-1, 0, -1], [1, -1, -1]], dtype=torch.int32, device="cuda")
+    C = torch.ones(2, 24, dtype=torch.bfloat16, device="cuda")
+    go = torch.full((2, 24), float("inf"), dtype=torch.bfloat16, device="cuda")
+    go[1] = float("nan")
+    w = torch.where(rows < 0, float("nan"), 1.0)
+    grad_w = fg.moe_combine_backward(go, C, rows, w)[1]
+    assert (grad_w[rows < 0] == 0).all() and torch.isinf(grad_w[0, 1]) and torch.isnan(grad_w[1, 0])
+    assert (fg.moe_combine(C, rows, w) == 1).all()
+
+
 def test_combine_rows_out_of_range_are_none(fg):
     C = torch.ones(4, 16, dtype=torch.bfloat16, device="cuda")
     rows = torch.tensor([[0, 4, -5], [2 ** 31 - 1, 3, 2]], dtype=torch.int32, device="cuda")
@@ -377,6 +389,9 @@ def test_lora_empty(fg):
     ids = torch.zeros(3, dtype=torch.int32, device="cuda")
     assert torch.equal(fg.lora_add(C, z(3, 16), z(0, 8, 16), z(0, 8, 8), ids), C)  # no adapters at all
     assert torch.equal(fg.lora_add(C, z(3, 16), z(2, 0, 16), z(2, 8, 0), ids), C)  # rank 0
+    big = torch.randn(100_000, 8, device="cuda").to(torch.bfloat16)
+    ids = torch.zeros(100_000, dtype=torch.int32, device="cuda")
+    assert torch.equal(fg.lora_add(big, z(100_000, 16), z(0, 8, 16), z(0, 8, 8), ids), big)
 
 
 # ------------------------------------------------------------------------------------- refusals

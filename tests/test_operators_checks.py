@@ -104,6 +104,8 @@ def test_combine_argument_errors():
     (dict(C=NULL), 1), (dict(x=NULL), 1), (dict(a=NULL), 1), (dict(b=NULL), 1), (dict(ids=NULL), 1), (dict(out=NULL), 1),
     (dict(M=-1), 1), (dict(L=-1), 1), (dict(K=24), 2), (dict(N=12), 2), (dict(R=12), 2), (dict(R=136), 3),
     (dict(x=P + 8), 2), (dict(out=P + 8), 2), (dict(scaling=P + 2), 2), (dict(M=0), 0), (dict(N=0), 0),
+    (dict(M=(1 << 24) + 1), 3), (dict(M=(1 << 18) + 1, L=1024), 3), (dict(L=0, out=P, x=NULL, a=NULL, b=NULL), 0),
+    (dict(R=0), 0), (dict(K=0), 0),
 ])
 def test_lora_argument_errors(change, expect):
     a = dict(C=P, x=P, a=P, b=P, ids=P, scaling=NULL, out=P, M=4, N=64, K=64, R=16, L=2, scratch=NULL, bytes=0,
