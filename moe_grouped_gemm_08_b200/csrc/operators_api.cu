@@ -192,7 +192,8 @@ size_t route_scratch_bytes(int S, int E, const RouteSplit& r) {
 
 // ------------------------------------------------------------------------------------ row layouts
 // How the pairs are split: one chunk (and one launch) up to 2048, then 512 a chunk while that leaves a CTA per
-// SM or fewer, else 2048.  (4096 pairs of 8 experts: 4.7 us in eight chunks, 5.9 us in one.)
+// SM or fewer, then 2048, and 8192 above a million, as every CTA reads all chunks' counts.  (4096 pairs of 8
+// experts: 4.7 us in eight chunks, 5.9 us in one.)
 struct LayoutSplit {
   int threads, items;
 };
@@ -200,7 +201,8 @@ LayoutSplit layout_split(long long pairs) {
   if (pairs <= 512) return {256, 2};
   if (pairs <= 2048) return {1024, 2};
   if (pairs <= 148 * 512) return {256, 2};
-  return {256, 8};
+  if (pairs <= 512 * 2048) return {256, 8};
+  return {1024, 8};
 }
 int layout_chunks(long long pairs) {
   const LayoutSplit s = layout_split(pairs);
@@ -212,16 +214,20 @@ fg_status layout_launch(const fg::LayoutParams& p, void* stream) {
   constexpr size_t most = THREADS / 32 * fg::kLayoutMaxExperts * 2;
   const size_t smem = static_cast<size_t>(THREADS / 32) * p.E * 2;
   if (!allow_smem<fg::moe_layout_kernel<THREADS, ITEMS>>(most)) return FG_ERR_CUDA;
-  if (p.chunks > 1) {
-    const fg_status s = launch(fg::moe_layout_count_kernel<THREADS, ITEMS>, dim3(p.chunks), THREADS, 0, stream, 1, p);
-    if (s != FG_OK) return s;
+  if constexpr (THREADS * ITEMS != 2048 || THREADS != 1024) {  // that split has one chunk
+    if (p.chunks > 1) {
+      const fg_status s = launch(fg::moe_layout_count_kernel<THREADS, ITEMS>, dim3(p.chunks), THREADS, 0, stream, 1, p);
+      if (s != FG_OK) return s;
+    }
   }
-  // a CTA per chunk, and at least one per 4096 rows of m_indices (256 experts, 512 pairs: 51 us with one)
-  const long long fill = cdiv(p.M, 4096);
-  long long ctas = p.chunks > fill ? p.chunks : fill < 128 ? fill : 128;
+  // a CTA per chunk, and one per 4096 rows of m_indices up to 128 (256 experts, 512 pairs: 51 us with one CTA)
+  long long ctas = cdiv(p.M, 4096);
+  if (ctas > 128) ctas = 128;
+  if (ctas < p.chunks) ctas = p.chunks;
   if (ctas < 1) ctas = 1;
   return launch(fg::moe_layout_kernel<THREADS, ITEMS>, dim3(static_cast<unsigned>(ctas)), THREADS, smem, stream, 1, p);
 }
+
 size_t layout_hist_bytes(long long pairs, int E) {
   const int chunks = layout_chunks(pairs);
   return chunks > 1 ? static_cast<size_t>(chunks) * E * 4 : 0;
@@ -230,7 +236,7 @@ size_t layout_hist_bytes(long long pairs, int E) {
 fg_status layout_run(fg::LayoutParams& p, void* stream) {
   p.chunks = layout_chunks(p.pairs);
   const LayoutSplit s = layout_split(p.pairs);
-  if (s.threads == 1024) return layout_launch<1024, 2>(p, stream);
+  if (s.threads == 1024) return s.items == 2 ? layout_launch<1024, 2>(p, stream) : layout_launch<1024, 8>(p, stream);
   return s.items == 2 ? layout_launch<256, 2>(p, stream) : layout_launch<256, 8>(p, stream);
 }
 

@@ -206,6 +206,30 @@ def test_layouts(fg, T, k, E, total):
             assert np.array_equal(masked_m.cpu().numpy(), want_m)
 
 
+@pytest.mark.parametrize("pairs,E", [(80_000, 256), (1_200_000, 1000), (300_000, 3)])
+def test_layouts_of_many_pairs(fg, pairs, E):
+    ids = torch.randint(-1, E + 1, (pairs, 1), generator=gen(pairs)).to(torch.int32)
+    flat = ids.flatten().numpy()
+    live = (flat >= 0) & (flat < E)
+    order = np.argsort(np.where(live, flat, E), kind="stable")
+    counts = np.bincount(flat[live], minlength=E)
+    place = np.empty(pairs, np.int64)
+    place[order] = np.arange(pairs)
+    place -= np.concatenate([[0], np.cumsum(counts)])[np.where(live, flat, E)]
+    padded = -(-counts // 128) * 128
+    start = np.cumsum(padded) - padded
+    rows, group = fg.moe_layout_contiguous(ids.cuda(), E)
+    assert np.array_equal(rows.cpu().numpy()[:, 0], np.where(live, start[np.clip(flat, 0, E - 1)] + place, -1))
+    want = np.full(group.numel(), -1, np.int32)
+    for e in range(E):
+        want[start[e]:start[e] + counts[e]] = e
+    assert np.array_equal(group.cpu().numpy(), want)
+    mmax = int(counts.max()) - 5
+    rows, masked_m = fg.moe_layout_masked(ids.cuda(), E, mmax)
+    assert np.array_equal(rows.cpu().numpy()[:, 0], np.where(live & (place < mmax), flat * mmax + place, -1))
+    assert np.array_equal(masked_m.cpu().numpy(), np.minimum(counts, mmax))
+
+
 def test_layout_without_pairs(fg):
     empty = torch.empty(0, 4, dtype=torch.int32, device="cuda")
     rows, group = fg.moe_layout_contiguous(empty, 8)
