@@ -323,12 +323,11 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (j >= p.k) break;
-        if (key[0] == best) {
-          keys[j] = best;
+        const bool wins = key[0] == best;
+        if (wins) keys[j] = best;
 #pragma unroll
-          for (int i = 0; i < (NPL < 7 - j ? NPL : 7 - j); ++i) key[i] = i + 1 < NPL ? key[i + 1] : K(0);
-        }
-        if (j + 1 < p.k) best = row_best<LPR>(key[0]);
+        for (int i = 0; i < (NPL < 7 - j ? NPL : 7 - j); ++i) key[i] = wins ? (i + 1 < NPL ? key[i + 1] : K(0)) : key[i];
+        best = row_best<LPR>(key[0]);
       }
     } else {
       for (int j = 0; j < p.k; ++j) {
