@@ -261,7 +261,7 @@ fg_status fg_moe_route(const void* logits, int dtype, const unsigned char* mask,
 
 /* Gradient of the router: grad_logits [S][T][E] (type of the logits, rounded once from fp32) from
  * grad_weights [S][T][k] and grad_loss [S], either NULL for none, with the ids and slope of the
- * forward call.  Tokens that were not routed (all ids -1) get zeros. */
+ * forward call with the same logits.  Tokens that were not routed (all ids -1) get zeros. */
 fg_status fg_moe_route_backward(const void* logits, int dtype, const int* ids, const float* slope,
                                 const float* grad_weights, const float* grad_loss, void* grad_logits, int S,
                                 int T, int E, int k, int renormalize, void* stream);
@@ -313,7 +313,8 @@ fg_status fg_moe_combine_backward(const void* grad_out, const void* C, const int
  * is rounded once.  K % 16 == 0, N % 8 == 0, R % 8 == 0, R <= 128 (a smaller rank is padded with
  * zeros), M <= 2^24, and M <= 2^18 with L >= FG_MOE_MAX_EXPERTS, else FG_ERR_UNSUPPORTED.  Rows of
  * one adapter may stand anywhere; many rows are first sorted by adapter, which takes the scratch
- * (16-byte aligned).  out overlaps C in whole or not at all, and no other operand.
+ * (16-byte aligned).  out overlaps C in whole or not at all, and no other operand.  lora_b must be
+ * finite (an infinity meets both parts that A_a x is split into).
  * A wait of a kernel for many rows that runs out (about two seconds) makes it write NaN and leave
  * FG_ERR_TIMEOUT for fg_lora_status, which synchronises `stream`, reads and clears it. */
 size_t fg_lora_scratch_bytes(int M, int R, int L);

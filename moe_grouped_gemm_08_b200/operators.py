@@ -109,7 +109,7 @@ def moe_combine_backward(grad_out, C, rows, weights, grad_C=None, stream=None):
 def lora_add(C, x, lora_a, lora_b, adapters, scaling=None, out=None, stream=None):
     """out[m] = C[m] + scaling[a] * lora_b[a] @ (lora_a[a] @ x[m]) with a = adapters[m] (int32 [M]; any
     value outside [0, L) leaves C[m]).  C bf16 [M, N], x bf16 [M, K], lora_a bf16 [L, R, K], lora_b bf16
-    [L, N, R], scaling float32 [L]; R a multiple of 8 up to 128.  out=C adds in place; None allocates."""
+    [L, N, R] (finite), scaling float32 [L]; R a multiple of 8 up to 128.  out=C adds in place; None allocates."""
     return _call(C, stream, _operators.lora_add, C, x, lora_a, lora_b, adapters, scaling, out)
 
 
