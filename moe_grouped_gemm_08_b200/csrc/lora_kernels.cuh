@@ -62,13 +62,15 @@ template <int NT>
 struct LoraRows {
   static constexpr int AHEAD = NT <= 2 ? 4 : NT <= 4 ? 2 : 1;  // blocks of K asked for at once
   static constexpr int CTAS = NT <= 4 ? 3 : NT <= 8 ? 2 : 1;   // per SM, for the registers
+  static constexpr int LD = NT * 8 + (NT >= 4 ? 8 : 0);  // row of h in shared memory, floats: padded against bank conflicts
+  static constexpr int SMEM = (kLoraWarps + 1) * 16 * LD * 4;
 };
 template <int NT, int CL>
 __global__ void __launch_bounds__(kLoraThreads, LoraRows<NT>::CTAS) lora_rows_kernel(const LoraParams p) {
-  constexpr int RP = NT * 8, AHEAD = LoraRows<NT>::AHEAD;
-  extern __shared__ float s_dyn[];
-  float* s_part = s_dyn;                          // [warps][16][RP], then the sum over the warps in [0]
-  float* s_h = s_dyn + kLoraWarps * 16 * RP;      // [16][RP]
+  constexpr int RP = NT * 8, AHEAD = LoraRows<NT>::AHEAD, LD = LoraRows<NT>::LD;
+  extern __shared__ __align__(16) float s_dyn[];
+  float* s_part = s_dyn;                      // [warps][16][LD], then the sum over the warps in [0]
+  float* s_h = s_dyn + kLoraWarps * 16 * LD;  // [16][LD]
   __shared__ int s_rows[16];
   __shared__ int s_cnt[kLoraWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -194,21 +196,24 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRows<NT>::CTAS) lora_rows_ke
   fetch(g0 + warp);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    float* part = s_part + warp * 16 * RP + n * 8 + q * 2;
-    *reinterpret_cast<float2*>(part + g * RP) = make_float2(acc[n][0], acc[n][1]);
-    *reinterpret_cast<float2*>(part + (g + 8) * RP) = make_float2(acc[n][2], acc[n][3]);
+    float* part = s_part + warp * 16 * LD + n * 8 + q * 2;
+    *reinterpret_cast<float2*>(part + g * LD) = make_float2(acc[n][0], acc[n][1]);
+    *reinterpret_cast<float2*>(part + (g + 8) * LD) = make_float2(acc[n][2], acc[n][3]);
   }
   const float scale = p.scaling ? p.scaling[ad] : 1.0f;
   __syncthreads();
-  for (int i = threadIdx.x; i < 16 * RP; i += kLoraThreads) {
-    float v = 0.0f;
+  for (int i = threadIdx.x; i < 16 * LD / 4; i += kLoraThreads) {  // (the rows' padding is summed along)
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-    for (int w = 0; w < kLoraWarps; ++w) v += s_part[w * 16 * RP + i];
-    s_part[i] = v;
+    for (int w = 0; w < kLoraWarps; ++w) {
+      const float4 t = *reinterpret_cast<const float4*>(s_part + w * 16 * LD + i * 4);
+      v = make_float4(v.x + t.x, v.y + t.y, v.z + t.z, v.w + t.w);
+    }
+    *reinterpret_cast<float4*>(s_part + i * 4) = v;
   }
   cluster_sync_all();
   const uint32_t part = smem_addr(s_part);
-  for (int i = threadIdx.x; i < 16 * RP / 4; i += kLoraThreads) {
+  for (int i = threadIdx.x; i < 16 * LD / 4; i += kLoraThreads) {
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int c = 0; c < CL; ++c) {
@@ -224,10 +229,12 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRows<NT>::CTAS) lora_rows_ke
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = s * 16 + q * 4 + (i >> 1) * 2, row = g + (i & 1) * 8;
-      const bool in = r < RP;
-      split_bf16x2(in ? s_h[row * RP + r] : 0.0f, in ? s_h[row * RP + r + 1] : 0.0f, hi[s][i], lo[s][i]);
+    for (int i = 0; i < 2; ++i) {  // four ranks of rows g and g + 8; ranks past the padded one are 0
+      const int r = s * 16 + q * 4;
+      const float4 v = r < RP ? *reinterpret_cast<const float4*>(s_h + (g + i * 8) * LD + r)
+                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      split_bf16x2(v.x, v.y, hi[s][i], lo[s][i]);
+      split_bf16x2(v.z, v.w, hi[s][i + 2], lo[s][i + 2]);
     }
   }
   for (int gr = g0 + warp; gr < g1; gr += kLoraWarps) {
@@ -279,7 +286,6 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRows<NT>::CTAS) lora_rows_ke
 constexpr int kLoraTileRows = 128;
 constexpr uint64_t kLoraWaitNs = 2000000000ull;  // far above any legal wait
 constexpr int kLoraTimeout = 6;                  // FG_ERR_TIMEOUT
-constexpr int kLoraLeastUnits = 8;               // K units that a CTA takes at least (bounds a tile's parts)
 
 template <int RP>
 struct LoraTile {
@@ -334,9 +340,13 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// CTAs of lora_down_kernel's grid that have units.
-__device__ __forceinline__ int lora_down_ctas(long long U, unsigned grid) {
-  const long long most = (U + kLoraLeastUnits - 1) / kLoraLeastUnits;
+// CTAs of lora_down_kernel's grid that have units: of U units, KB a tile, each takes at least about sqrt(3/4 KB).  A
+// unit costs its CTA 0.4 us and a part of a tile's h its readers 0.3, so that a tile of KB units is best
+// cut into about sqrt(4/3 KB) parts (KB = 3: 2, 112: 12) where there are CTAs enough.
+__device__ __forceinline__ int lora_down_ctas(long long U, int KB, unsigned grid) {
+  long long least = 1;
+  while (4 * least * least < 3ll * KB) ++least;
+  const long long most = (U + least - 1) / least;
   return static_cast<int>(most < grid ? most : grid);
 }
 
@@ -373,7 +383,7 @@ __global__ void __launch_bounds__(kLoraThreads, LoraTile<RP>::CTAS) lora_down_ke
   pdl_launch_dependents();
   const int KB = (p.K + 63) / 64;
   const long long U = static_cast<long long>(p.tiles[0]) * KB;
-  const int P = lora_down_ctas(U, gridDim.x);
+  const int P = lora_down_ctas(U, KB, gridDim.x);
   if (static_cast<int>(blockIdx.x) >= P) return;
   const int u0 = lora_begin(blockIdx.x, P, U), n = lora_begin(blockIdx.x + 1, P, U) - u0;
   if (warp == 0) {
@@ -538,7 +548,7 @@ __global__ void __launch_bounds__(kLoraThreads, LoraTile<RP>::CTAS) lora_up_kern
   const int chunks = (p.N + 63) / 64;
   const int KB = (p.K + 63) / 64;
   const long long U = static_cast<long long>(__ldcg(p.tiles)) * KB;
-  const int PU = lora_down_ctas(U, gridDim.x);  // the grid of lora_down_kernel, as large as this one
+  const int PU = lora_down_ctas(U, KB, gridDim.x);  // the grid of lora_down_kernel, as large as this one
   const long long V = static_cast<long long>(__ldcg(p.tiles)) * chunks;
   const int P = static_cast<int>(V < gridDim.x ? V : gridDim.x);
   int v = 0, v_end = 0;

@@ -268,7 +268,7 @@ fg_status layout_check(const int* ids, const int* rows, const int* group, long l
 
 template <int NT, int CL>
 fg_status lora_rows_launch(const fg::LoraParams& p, void* stream) {
-  constexpr size_t smem = static_cast<size_t>(fg::kLoraWarps + 1) * 16 * NT * 8 * 4;
+  constexpr size_t smem = fg::LoraRows<NT>::SMEM;
   if (!allow_smem<fg::lora_rows_kernel<NT, CL>>(smem)) return FG_ERR_CUDA;
   return launch(fg::lora_rows_kernel<NT, CL>, dim3(static_cast<unsigned>(p.M) * CL), fg::kLoraThreads, smem, stream, CL, p);
 }
