@@ -246,9 +246,9 @@ typedef enum { FG_F32 = 0, FG_BF16 = 1, FG_F16 = 2 } fg_dtype;
  * its logits over all E: ids [S][T][k] int32 are the k largest logits, largest first, the lowest
  * expert first among equals; weights [S][T][k] are p at the ids, divided by their sum when
  * `renormalize`.  A logit of -inf or NaN is never chosen: choices that are left over have id -1
- * and weight 0, and a token without any choice is not routed.  (NaN and +inf logits of a routed
- * token still make its weights and the loss NaN, as the softmax does.)  Per sequence, over its n
- * routed tokens: counts [S][E], the choices of each expert; with f = counts / sum(counts) and P
+ * and weight 0, and a token without any choice is not routed.  (A NaN or +inf logit of a routed
+ * token makes the loss NaN, as it does the softmax, and may make the token's weights NaN; its ids
+ * stay k different experts or -1.)  Per sequence, over its n routed tokens: counts [S][E], the choices of each expert; with f = counts / sum(counts) and P
  * the mean of p: loss [S] = E * sum_e f_e P_e (1 for an even load; 0 with n = 0) and
  * slope [S][E] = E f_e / n, the derivative of the loss by each token's p (counts are not
  * differentiated), for the backward pass.  Sums are fp32.  1 <= k <= min(E, 32),
