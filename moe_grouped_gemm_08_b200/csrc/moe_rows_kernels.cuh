@@ -177,14 +177,14 @@ __global__ void __launch_bounds__(THREADS) moe_layout_kernel(const LayoutParams 
   }
   // m_indices, four rows at a time (a block is a multiple of four): the last expert whose block starts at or
   // before the row, if the row holds one of its pairs (experts without pairs share their start with the
-  // next one and are passed over)
-  for (int r = (blockIdx.x * THREADS + threadIdx.x) * 4; r < p.M; r += gridDim.x * THREADS * 4) {
+  // next one and are passed over).  r in 64 bits: M may be the largest int.
+  for (long long r = (blockIdx.x * THREADS + threadIdx.x) * 4; r < p.M; r += gridDim.x * THREADS * 4) {
     int lo = 0, hi = p.E;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (s_start[mid] <= r) lo = mid; else hi = mid;
     }
-    const int left = s_start[lo] + s_count[lo] - r;
+    const int left = static_cast<int>(s_start[lo] + s_count[lo] - r);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (r + i < p.M) p.group[r + i] = i < left ? lo : -1;

@@ -1,0 +1,43 @@
+"""GPU tests of the operators around the GEMMs at the top of the sizes that they accept: row and column
+numbers next to 2^31.  Sums and values are chosen to be exact, so that nothing here has a tolerance
+unless it says so."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fg():
+    import moe_grouped_gemm_08_b200 as lib
+    torch.cuda.set_device(0)
+    lib.init(0)
+    return lib
+
+
+@pytest.fixture(autouse=True)
+def _give_back_memory():
+    yield
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("pairs", [10, 100_000])
+def test_contiguous_layout_of_the_most_rows(fg, pairs):
+    """m_indices of 2^31 - 1 rows, as the C ABI takes them: every row is written, and nothing in front."""
+    M, E, front = 2 ** 31 - 1, 3, 1 << 23
+    ids = torch.arange(pairs, device="cuda", dtype=torch.int32) % E
+    rows = torch.empty_like(ids)
+    buffer = torch.full((front + M,), 77, dtype=torch.int32, device="cuda")
+    scratch = torch.empty(max(fg.lib.fg_moe_layout_scratch_bytes(pairs, E), 4), dtype=torch.uint8, device="cuda")
+    code = fg.lib.fg_moe_layout_contiguous(ids.data_ptr(), rows.data_ptr(), buffer[front:].data_ptr(), pairs, E, M,
+                                           scratch.data_ptr(), scratch.numel(), torch.cuda.current_stream().cuda_stream)
+    assert code == 0
+    torch.cuda.synchronize()
+    want_rows, want = fg.moe_layout_contiguous(ids, E)
+    assert torch.equal(rows, want_rows)
+    assert bool((buffer[:front] == 77).all())
+    group = buffer[front:]
+    assert torch.equal(group[:want.numel()], want)
+    assert bool((group[want.numel():] == -1).all())
