@@ -269,9 +269,9 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
   float acc[NPL];
 #pragma unroll
   for (int i = 0; i < NPL; ++i) acc[i] = 0.0f;
-  const int first = chunk * p.rows_per_chunk;
-  const int last = min(p.T, first + p.rows_per_chunk);
-  const size_t base = static_cast<size_t>(seq) * p.T;
+  // rows are counted from the chunk's first one, so that row numbers next to 2^31 do not overflow
+  const int first = chunk * p.rows_per_chunk, last = min(p.T - first, p.rows_per_chunk);
+  const size_t base = static_cast<size_t>(seq) * p.T + first;
   const T* logits = static_cast<const T*>(p.logits) + base * p.E;
   const uint8_t* mask = p.mask ? p.mask + base : nullptr;
   int* ids = p.ids + base * p.k;
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
     load_logits<T, LPR, NPL, V>(logits + static_cast<size_t>(r) * p.E, p.E, sub, next);
   };
   K* keys = s_key[warp][rw];
-  int r0 = first + warp * RPW;
+  int r0 = warp * RPW;
   if (r0 < last) fetch(r0);
   for (; r0 < last; r0 += kRouteWarps * RPW) {
     const int r = r0 + rw;
@@ -519,9 +519,9 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_backward_kernel(const
     const int c = route_col<LPR, V>(i, sub);
     h[i] = p.grad_loss && c < p.E ? g * p.slope[static_cast<size_t>(seq) * p.E + c] : 0.0f;
   }
-  const int first = blockIdx.x * p.rows_per_chunk;
-  const int last = min(p.T, first + p.rows_per_chunk);
-  const size_t base = static_cast<size_t>(seq) * p.T;
+  // as in the forward kernel, rows from the chunk's first one
+  const int first = blockIdx.x * p.rows_per_chunk, last = min(p.T - first, p.rows_per_chunk);
+  const size_t base = static_cast<size_t>(seq) * p.T + first;
   const T* all = static_cast<const T*>(p.logits) + base * p.E;
   T* out_all = static_cast<T*>(p.grad_logits) + base * p.E;
   const int* ids = p.ids + base * p.k;
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_backward_kernel(const
     load_logits<T, LPR, NPL, V>(all + static_cast<size_t>(r) * p.E, p.E, sub, next);
     if (sub < p.k) choice(r, sub, next_id, next_g);
   };
-  int r0 = first + warp * RPW;
+  int r0 = warp * RPW;
   if (r0 < last) fetch(r0);
   for (; r0 < last; r0 += kRouteWarps * RPW) {
     const int r = min(r0 + rw, last - 1);

@@ -41,3 +41,31 @@ def test_contiguous_layout_of_the_most_rows(fg, pairs):
     group = buffer[front:]
     assert torch.equal(group[:want.numel()], want)
     assert bool((group[want.numel():] == -1).all())
+
+
+@pytest.mark.parametrize("masked", [False, True])
+def test_router_of_the_most_tokens(fg, masked):
+    """2^31 - 1 tokens of one sequence and one expert: each takes it with weight 1, and its logit has no
+    gradient.  (A chunk's sum of p holds at most 2^24 ones exactly; the sum of the chunks', eight per SM, and
+    the division lose up to 1000 roundings of 2^-24.)"""
+    T = 2 ** 31 - 1
+    logits = torch.zeros(T, 1, dtype=torch.bfloat16, device="cuda")
+    mask = None
+    if masked:
+        mask = torch.ones(T, dtype=torch.bool, device="cuda")
+        mask[-1000:-1] = False
+    routed = T - 999 * masked
+    ids, weights, counts, loss, slope = fg.moe_route(logits, 1, mask=mask)
+    assert counts.tolist() == [routed]
+    assert abs(loss.item() - 1.0) <= 1000 * 2.0 ** -24
+    assert abs(slope.item() * routed - 1.0) <= 4 * 2.0 ** -24
+    for part, want in ((ids, 0), (weights, 1)):
+        live, dead = (part[:T - 1000], part[T - 1000:T - 1]) if masked else (part, part[:0])
+        assert bool((live == want).all()) and bool((part[-1:] == want).all())
+        assert bool((dead == want - 1).all())  # id -1, weight 0
+    del weights
+    grad = fg.moe_route_backward(logits, ids, slope, None, torch.ones((), device="cuda"))
+    assert not bool(grad.any())
+    grad.fill_(1.0)
+    del grad
+    assert not bool(fg.moe_route_backward(logits, ids, slope, None, torch.ones((), device="cuda")).any())
