@@ -438,8 +438,9 @@ __global__ void __launch_bounds__(kCombineGradThreads, 3) moe_combine_backward_k
     const float mw = w_next;
     if (item + gridDim.x < items) fetch(item + gridDim.x);
     float dot[8] = {};
-    for (int c0 = 0; c0 < p.N; c0 += V * SPAN) {
-      const int col0 = c0 + threadIdx.x * 8;
+    // unsigned: the step past the last columns may reach 2^31, at which V SPAN ends a pass exactly
+    for (unsigned c0 = 0; c0 < static_cast<unsigned>(p.N); c0 += V * SPAN) {
+      const int col0 = static_cast<int>(c0) + threadIdx.x * 8;
       const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
       uint4 graw[V], raw[V][J];
 #pragma unroll

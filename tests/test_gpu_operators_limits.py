@@ -69,3 +69,31 @@ def test_router_of_the_most_tokens(fg, masked):
     grad.fill_(1.0)
     del grad
     assert not bool(fg.moe_route_backward(logits, ids, slope, None, torch.ones((), device="cuda")).any())
+
+
+@pytest.mark.parametrize("k", [1, 4, 5])
+def test_combine_gradient_of_the_widest_rows(fg, k):
+    """Rows of 2^31 - 8 columns, zero but for a few at both ends and between.  Every pass of the gradient's kernel over
+    the columns (8192, 4096 or 2048 wide by k) ends at 2^31."""
+    N = 2 ** 31 - 8
+    at = torch.tensor([0, 7, 8191, 8192, 2 ** 30 + 5, N - 8193, N - 8184, N - 1], device="cuda")
+    values = torch.arange(1, 9, device="cuda")
+    C = torch.zeros(2, N, dtype=torch.bfloat16, device="cuda")
+    C[1, at] = values.to(torch.bfloat16)
+    grad_out = torch.zeros(1, N, dtype=torch.bfloat16, device="cuda")
+    grad_out[0, at] = 2.0
+    rows = torch.full((1, k), -1, dtype=torch.int32, device="cuda")
+    rows[0, -1] = 1
+    weights = torch.full((1, k), 0.5, device="cuda")
+    grad_C = torch.full((2, N), 3.0, dtype=torch.bfloat16, device="cuda")
+    _, grad_w = fg.moe_combine_backward(grad_out, C, rows, weights, grad_C=grad_C)
+    assert grad_w[0].tolist() == [0.0] * (k - 1) + [72.0]
+    assert bool((grad_C[0] == 3.0).all())
+    assert bool((grad_C[1, at] == 1.0).all())
+    grad_C[1, at] = 0.0
+    assert not bool(grad_C[1].any())
+    del grad_C, grad_out
+    out = fg.moe_combine(C, rows, weights)
+    assert torch.equal(out[0, at].float(), values * 0.5)
+    out[0, at] = 0.0
+    assert not bool(out.any())
