@@ -240,7 +240,7 @@ template <int FMT>
 __global__ void __launch_bounds__(256) moe_dispatch_kernel(const DispatchParams p, int chunks) {
   const int lane = threadIdx.x & 31;
   const long long nwarps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
-  const int KB = (p.K + 127) / 128;
+  const int KB = (p.K - 1) / 128 + 1;  // K > 0, and K + 127 may not fit
   pdl_wait_prior_grid();
   pdl_launch_dependents();
   for (long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; w < p.T * chunks;

@@ -97,3 +97,21 @@ def test_combine_gradient_of_the_widest_rows(fg, k):
     assert torch.equal(out[0, at].float(), values * 0.5)
     out[0, at] = 0.0
     assert not bool(out.any())
+
+
+def test_dispatch_of_the_widest_rows(fg):
+    """Rows of 2^31 - 16 columns, the last block of them partial: codes and scales at both ends."""
+    K = 2 ** 31 - 16
+    x = torch.zeros(1, K, dtype=torch.bfloat16, device="cuda")
+    x[0, 0], x[0, 1], x[0, K - 1], x[0, K - 2] = 448.0, -7.0, 896.0, 3.5
+    rows = torch.tensor([[2, -1]], dtype=torch.int32, device="cuda")
+    A = torch.full((4, K), 0xA5, dtype=torch.uint8, device="cuda")
+    sfa = torch.full((2 ** 24, 4), -7.0, device="cuda")
+    fg.moe_dispatch_fp8(x, rows, A=A, sfa=sfa)
+    for other in (0, 1, 3):
+        assert bool((A[other] == 0xA5).all()) and bool((sfa[:, other] == -7.0).all())
+    codes = A[2].view(torch.float8_e4m3fn)
+    assert codes[:2].float().tolist() == [448.0, -7.0] and codes[-2:].float().tolist() == [1.75, 448.0]
+    assert int((A[2] != 0).sum()) == 4
+    scale = sfa[:, 2]
+    assert scale[0].item() == 1.0 and scale[-1].item() == 2.0 and bool((scale[1:-1] == 1.0).all())
