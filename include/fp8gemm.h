@@ -288,7 +288,9 @@ fg_status fg_moe_layout_masked(const int* ids, int* rows, int* masked_m, long lo
  * x bf16 [T][K], rows [T][k]; A [G][M][K] codes and sfa [G][ceil(K/128)][fg_sfa_ld(M)]:
  * G = 1 and M = all rows for the contiguous layout, G = E and M = mmax for the masked one.  Rows
  * that no pair has keep their contents.  No row may stand in `rows` twice (rows of
- * fg_moe_layout_* never do).  K % 16 == 0, k <= 32, G * M < 2^31; x must be finite. */
+ * fg_moe_layout_* never do).  K % 16 == 0, k <= 32, G * M < 2^31, M <= FG_MOE_MAX_ROWS (above it
+ * fg_sfa_ld(M) is no int); x must be finite. */
+#define FG_MOE_MAX_ROWS 0x7ffffffc
 fg_status fg_moe_dispatch_fp8(const void* x, const int* rows, void* A, float* sfa, int T, int k, int G, int M,
                               int K, int fmt, void* stream);
 

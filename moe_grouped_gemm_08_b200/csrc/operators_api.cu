@@ -455,7 +455,7 @@ fg_status fg_moe_dispatch_fp8(const void* x, const int* rows, void* A, float* sf
   if (!x || !rows || !A || !sfa) return FG_ERR_INVALID_ARG;
   if (K % 16 != 0 || !aligned(x, 16) || !aligned(A, 16) || !aligned(sfa, 4) || !aligned(rows, 4))
     return FG_ERR_ALIGNMENT;
-  if (k > fg::kRowsMaxK || static_cast<long long>(G) * M > 0x7fffffffll) return FG_ERR_UNSUPPORTED;
+  if (k > fg::kRowsMaxK || static_cast<long long>(G) * M > 0x7fffffffll || M > FG_MOE_MAX_ROWS) return FG_ERR_UNSUPPORTED;
   fg::DispatchParams p;
   p.x = static_cast<const __nv_bfloat16*>(x);
   p.rows = rows;

@@ -284,6 +284,7 @@ PyObject* moe_dispatch_fp8(PyObject* const* a) {
   }
   if (lead.size() != 1 && lead.size() != 2) raise(PyExc_ValueError, "the layout is M rows or (G, Mmax)");
   const int M = to_int(lead.back(), "the layout"), G = lead.size() == 2 ? to_int(lead[0], "the layout") : 1;
+  if (M > FG_MOE_MAX_ROWS) raise(PyExc_ValueError, "the layout is too large");
   const auto scales = joined(at::IntArrayRef(lead).slice(0, lead.size() - 1), {(static_cast<int64_t>(K) + 127) / 128, fg_sfa_ld(M)});
   const auto codes = joined(lead, {K});
   Tensor A, sfa;
