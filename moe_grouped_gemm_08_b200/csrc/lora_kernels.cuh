@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRows<NT>::CTAS) lora_rows_ke
   }
   __syncthreads();
   const int row0 = s_rows[g], row1 = s_rows[g + 8];
-  const int groups = (p.N + 31) / 32;
+  const int groups = (p.N - 1) / 32 + 1;  // N > 0, and N + 31 may not fit; so for K
   const int g0 = static_cast<int>(static_cast<long long>(groups) * rank / CL);
   const int g1 = static_cast<int>(static_cast<long long>(groups) * (rank + 1) / CL);
 
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRows<NT>::CTAS) lora_rows_ke
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-  const int kblocks = (p.K + 31) / 32;
+  const int kblocks = (p.K - 1) / 32 + 1;
   const int k0 = static_cast<int>(static_cast<long long>(kblocks) * rank / CL);
   const int k1 = static_cast<int>(static_cast<long long>(kblocks) * (rank + 1) / CL);
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);

@@ -115,3 +115,34 @@ def test_dispatch_of_the_widest_rows(fg):
     assert int((A[2] != 0).sum()) == 4
     scale = sfa[:, 2]
     assert scale[0].item() == 1.0 and scale[-1].item() == 2.0 and bool((scale[1:-1] == 1.0).all())
+
+
+def test_adapter_of_the_widest_rows(fg):
+    """K = 2^31 - 16, then N = 2^31 - 8, the other small: few values beside zeros, at both ends."""
+    K, N, R = 2 ** 31 - 16, 16, 8
+    ids = torch.zeros(1, dtype=torch.int32, device="cuda")
+    at = torch.tensor([0, 31, 32, 2 ** 30 + 3, K - 33, K - 1], device="cuda")
+    x = torch.zeros(1, K, dtype=torch.bfloat16, device="cuda")
+    x[0, at] = torch.arange(1.0, 7.0, device="cuda").to(torch.bfloat16)
+    a = torch.zeros(1, R, K, dtype=torch.bfloat16, device="cuda")
+    for r in range(R):
+        a[0, r, at] = r + 1.0
+    b = torch.zeros(1, N, R, dtype=torch.bfloat16, device="cuda")
+    b[0, :, 0], b[0, 3, 7] = 1.0, 1.0
+    C = torch.ones(1, N, dtype=torch.bfloat16, device="cuda")
+    out = fg.lora_add(C, x, a, b, ids)[0]
+    want = torch.full((N,), 22.0)
+    want[3] += 168.0
+    assert torch.equal(out.float().cpu(), want)
+    del a, x
+    N = 2 ** 31 - 8
+    at = torch.tensor([0, 31, 32, 2 ** 30 + 3, N - 33, N - 1], device="cuda")
+    b = torch.zeros(1, N, R, dtype=torch.bfloat16, device="cuda")
+    b[0, at, 2] = torch.arange(1.0, 7.0, device="cuda").to(torch.bfloat16)
+    x = torch.ones(1, 16, dtype=torch.bfloat16, device="cuda")
+    a = torch.full((1, R, 16), 0.25, dtype=torch.bfloat16, device="cuda")
+    C = torch.zeros(1, N, dtype=torch.bfloat16, device="cuda")
+    out = fg.lora_add(C, x, a, b, ids)[0]
+    assert out[at].tolist() == [4.0 * i for i in range(1, 7)]
+    out[at] = 0.0
+    assert not bool(out.any())
