@@ -220,14 +220,18 @@ struct RouteParams {
 // What the sums over a sequence give.  Called by all threads of one CTA; thread e < E holds column e's
 // sum of p and count; rows: the routed tokens (same in every thread).
 __device__ __forceinline__ void route_finish(const RouteParams& p, int seq, float sum, int n, int rows, float* s_red,
-                                             int* s_total) {
+                                             unsigned long long* s_total) {
   const int e = threadIdx.x, warps = blockDim.x / 32;
-  const int here = __reduce_add_sync(0xffffffffu, e < p.E ? n : 0);
+  // all choices of the sequence, T k of them, may pass 2^32: a warp sums the halves of its counts apart
+  const uint32_t mine = e < p.E ? n : 0;
+  const unsigned long long here =
+      (static_cast<unsigned long long>(__reduce_add_sync(0xffffffffu, mine >> 16)) << 16) +
+      __reduce_add_sync(0xffffffffu, mine & 0xffffu);
   if (e == 0) *s_total = 0;
   __syncthreads();
   if ((e & 31) == 0 && here) atomicAdd(s_total, here);
   __syncthreads();
-  const float total = static_cast<float>(max(*s_total, 1)) * static_cast<float>(max(rows, 1));
+  const float total = static_cast<float>(max(*s_total, 1ull)) * static_cast<float>(max(rows, 1));
   const float slope = static_cast<float>(p.E) * static_cast<float>(n) / total;
   if (e < p.E) {
     p.counts[static_cast<size_t>(seq) * p.E + e] = n;
@@ -398,7 +402,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
   }
   if constexpr (CLUSTER) {
     __shared__ float s_red[kRouteWarps];
-    __shared__ int s_total;
+    __shared__ unsigned long long s_total;
     cluster_sync_all();
     if (chunk == 0) {
       static_assert(EP <= kRouteThreads, "one column per thread");
@@ -431,7 +435,8 @@ __global__ void __launch_bounds__(1024) moe_route_finish_kernel(const RouteParam
   __shared__ float s_part[1024];
   __shared__ int s_cnt[1024];
   __shared__ float s_red[32];
-  __shared__ int s_total, s_rows;
+  __shared__ unsigned long long s_total;
+  __shared__ int s_rows;
   const int seq = blockIdx.y, rank = static_cast<int>(cluster_ctarank());
   if (threadIdx.x == 0) s_rows = 0;
   __syncthreads();

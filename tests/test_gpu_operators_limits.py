@@ -146,3 +146,15 @@ def test_adapter_of_the_widest_rows(fg):
     assert out[at].tolist() == [4.0 * i for i in range(1, 7)]
     out[at] = 0.0
     assert not bool(out.any())
+
+
+@pytest.mark.parametrize("T,E,k", [(2 ** 27, 16, 16), (2 ** 27 + 5, 32, 32)])
+def test_balance_loss_of_more_choices_than_2_to_the_31(fg, T, E, k):
+    """Every token takes every expert: an even load, whose loss is 1 and whose slope E f / n is 1 / n.  (p is 1 / E
+    exactly; its sums over a chunk are exact, and the sum of eight chunks per SM loses up to 1300 u.)"""
+    ids, weights, counts, loss, slope = fg.moe_route(torch.zeros(T, E, dtype=torch.bfloat16, device="cuda"), k)
+    assert bool((ids == torch.arange(E, device="cuda", dtype=torch.int32)).all())
+    assert bool((weights == 1.0 / E).all())
+    assert counts.tolist() == [T] * E
+    assert bool(((slope * T - 1.0).abs() <= 4 * 2.0 ** -24).all())
+    assert abs(loss.item() - 1.0) <= 1300 * 2.0 ** -24
