@@ -325,6 +325,11 @@ fg_status fg_lora_add(const void* C, const void* x, const void* lora_a, const vo
                       void* scratch, size_t scratch_bytes, void* stream);
 fg_status fg_lora_status(void* stream);
 
+/* Failure injection for tests (process-wide, default 0): with 1 or 2, every CTA of the first or second
+ * kernel of fg_lora_add for many rows first waits for a product that it has not issued, and issues none after
+ * that wait has run out.  Nothing faults, and the context stays usable.  Returns the previous value. */
+int fg_lora_debug_set_stall(int kernel);
+
 /* Synchronise `stream`, then read and clear the device status word:
  * FG_OK, or FG_ERR_TIMEOUT if some kernel since the last call gave up a wait, or (debug
  * build, libfp8gemm_debug.so, compiled with -DFG_DEBUG) FG_ERR_DEVICE_CHECK if a

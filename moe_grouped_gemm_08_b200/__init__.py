@@ -135,6 +135,8 @@ def _declare(l: ctypes.CDLL) -> ctypes.CDLL:
     l.fg_lora_add.restype = _int
     l.fg_lora_status.argtypes = [_vp]
     l.fg_lora_status.restype = _int
+    l.fg_lora_debug_set_stall.argtypes = [_int]
+    l.fg_lora_debug_set_stall.restype = _int
     l.fg_launch_count.argtypes = []
     l.fg_launch_count.restype = ctypes.c_uint64
     return l

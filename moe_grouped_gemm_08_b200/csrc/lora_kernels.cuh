@@ -30,6 +30,7 @@ struct LoraParams {
   const int* tiles;      // tiles of adapters, tiles in all
   float* parts;          // [2 * CTAs + tiles][rank padded / 4][128][4]: two parts of h per CTA, whole h per tile
   int* status;
+  int stall;  // test hook: the products' thread of lora_down_kernel (1) or lora_up_kernel (2) first waits for nothing
 };
 
 // D += A B, one 16 x 8 x 16 bf16 product of a warp with fp32 accumulators.
@@ -434,6 +435,8 @@ __global__ void __launch_bounds__(kLoraThreads, LoraTile<RP>::CTAS) lora_down_ke
     load();
   };
   bool ok = true;
+  // (the test hook: no product has been issued, so this wait runs out)
+  if (p.stall == 1 && tid == 0) ok = mbar_wait(&done[0], 0, &s_abort, kLoraWaitNs);
 #pragma unroll 1
   for (int it = 0; it < STAGES - 1; ++it) {
     if (it == 0)
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(kLoraThreads, LoraTile<RP>::CTAS) lora_down_ke
     cp_async_wait<STAGES - 2>();
     fence_proxy_async_smem();
     __syncthreads();
-    if (tid == 0) {
+    if (tid == 0 && ok) {
       tc_fence_after();
       const uint32_t st = base + (it % STAGES) * L::STAGE_BYTES;
       const uint64_t adesc = smem_desc_k128_sw128(st), bdesc = smem_desc_k128_sw128(st + L::X_BYTES);
@@ -558,6 +561,7 @@ __global__ void __launch_bounds__(kLoraThreads, LoraTile<RP>::CTAS) lora_up_kern
   }
   int row[4];
   bool ok = true, waited = false;
+  if (p.stall == 2 && tid == 0) ok = mbar_wait(&done[0], 0, &s_abort, kLoraWaitNs);  // as in lora_down_kernel
   int used = 0;  // products so far: the TMEM buffer and the phase of its barrier go by it
   while (v < v_end) {
     const int t = v / chunks, c0 = v - t * chunks;
@@ -595,6 +599,10 @@ __global__ void __launch_bounds__(kLoraThreads, LoraTile<RP>::CTAS) lora_up_kern
       tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (use & 1) * 64 + half * 32, d);
       tmem_wait_ld();
       tc_fence_before();
+      if (!ok) {  // NaN after a wait that ran out
+#pragma unroll
+        for (int i = 0; i < 32; ++i) d[i] = 0x7fffffffu;
+      }
       const uint32_t cs = base + C_RING + (c % RING) * L::X_BYTES;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -670,7 +678,7 @@ __global__ void __launch_bounds__(kLoraThreads, LoraTile<RP>::CTAS) lora_up_kern
       cp_async_wait<RING - 2>();
       fence_proxy_async_smem();
       __syncthreads();
-      if (tid == 0) {
+      if (tid == 0 && ok) {
         tc_fence_after();
         const uint32_t d = tmem + ((used + c) & 1) * 64;
 #pragma unroll

@@ -317,6 +317,8 @@ LoraScratch lora_scratch(int M, int L, int R, int sms) {
   return s;
 }
 
+std::atomic<int> g_lora_stall{0};  // fg_lora_debug_set_stall
+
 __device__ int g_lora_status;  // FG_ERR_TIMEOUT once a wait of the kernels for many rows has run out
 
 // Its address, looked up once per device (not again during a capture).
@@ -581,6 +583,7 @@ fg_status fg_lora_add(const void* C, const void* x, const void* lora_a, const vo
     if (sms <= 0) return FG_ERR_CUDA;
     const LoraScratch need = lora_scratch(M, L, R, sms);
     if (!scratch || scratch_bytes < need.bytes) return FG_ERR_INVALID_ARG;
+    p.stall = g_lora_stall.load(std::memory_order_relaxed);
     p.status = lora_status_word();
     if (!p.status) return FG_ERR_CUDA;
     uint8_t* at = static_cast<uint8_t*>(scratch);
@@ -613,6 +616,8 @@ fg_status fg_lora_add(const void* C, const void* x, const void* lora_a, const vo
   if (R <= 64) return lora_rows_pick<8>(p, stream);
   return lora_rows_pick<16>(p, stream);
 }
+
+int fg_lora_debug_set_stall(int kernel) { return g_lora_stall.exchange(kernel == 1 || kernel == 2 ? kernel : 0); }
 
 fg_status fg_lora_status(void* stream) {
   int* at = lora_status_word();
