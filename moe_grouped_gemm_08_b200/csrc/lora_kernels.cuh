@@ -221,7 +221,9 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRows<NT>::CTAS) lora_rows_ke
       const float4 w = ld_dsmem_f4(mapa_shared(part + i * 16, c));
       v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
     }
-    *reinterpret_cast<float4*>(s_h + i * 4) = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
+    // ranks that only pad are 0 even where x (times the 0 of A) made a NaN of them
+    *reinterpret_cast<float4*>(s_h + i * 4) =
+        i * 4 % LD < p.R ? make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   }
   cluster_sync_all();  // every rank has read the parts; s_h is complete
 
@@ -641,7 +643,7 @@ __global__ void __launch_bounds__(kLoraThreads, LoraTile<RP>::CTAS) lora_up_kern
     }
     {  // h (its last product of the tile before has run: every thread has waited for it)
       const int first = lora_owner(t * KB, PU, U), last = lora_owner(t * KB + KB - 1, PU, U);
-      const float scale = p.scaling ? p.scaling[ad] : 1.0f;
+      const float adapter_scale = p.scaling ? p.scaling[ad] : 1.0f;
       constexpr int EACH = L::PART_FLOATS / 4 / kLoraThreads, SIDE = EACH < 8 ? EACH : 8;  // quads of a thread; at once
 #pragma unroll 1
       for (int e = 0; e < EACH; e += SIDE) {
@@ -664,6 +666,8 @@ __global__ void __launch_bounds__(kLoraThreads, LoraTile<RP>::CTAS) lora_up_kern
         for (int i = 0; i < SIDE; ++i) {
           const int at = (e + i) * kLoraThreads + tid, m = at % kLoraTileRows, r = at / kLoraTileRows * 4;
           uint32_t hi[2], lo[2];
+          if (r >= p.R) h[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // padding, which infinities in x make NaN
+          const float scale = r < p.R ? adapter_scale : 0.0f;
           split_bf16x2(h[i].x * scale, h[i].y * scale, hi[0], lo[0]);
           split_bf16x2(h[i].z * scale, h[i].w * scale, hi[1], lo[1]);
           const uint32_t dst =
