@@ -311,12 +311,12 @@ fg_status fg_moe_combine_backward(const void* grad_out, const void* C, const int
 /* Low-rank adapters beside a projection: out[m] = C[m] + scaling[a] * B_a (A_a x[m]), a =
  * adapters[m] in [0, L); any other value leaves out[m] = C[m].  C, out bf16 [M][N] (out may be C),
  * x bf16 [M][K], lora_a bf16 [L][R][K], lora_b bf16 [L][N][R], scaling fp32 [L] or NULL (all 1).
- * Both products accumulate in fp32, A_a x is kept to 16 bits of mantissa between them, and the sum
+ * Both products accumulate in fp32, A_a x keeps its fp32 values between them, and the sum
  * is rounded once.  K % 16 == 0, N % 8 == 0, R % 8 == 0, R <= 128 (a smaller rank is padded with
  * zeros), M <= 2^24, and M <= 2^18 with L >= FG_MOE_MAX_EXPERTS, else FG_ERR_UNSUPPORTED.  Rows of
  * one adapter may stand anywhere; many rows are first sorted by adapter, which takes the scratch
  * (16-byte aligned).  out overlaps C in whole or not at all, and no other operand.  lora_b must be
- * finite (an infinity meets both parts that A_a x is split into).
+ * finite (an infinity meets each of the parts that A_a x is split into).
  * A wait of a kernel for many rows that runs out (about two seconds) makes it write NaN and leave
  * FG_ERR_TIMEOUT for fg_lora_status, which synchronises `stream`, reads and clears it. */
 size_t fg_lora_scratch_bytes(int M, int R, int L);

@@ -41,14 +41,19 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// (hi, lo) bf16 pairs of two fp32 values: hi + lo is within 2^-16 of the value, relative.  An
-// infinity or a NaN stays in hi alone (inf - inf would make a NaN of lo).
-__device__ __forceinline__ float bf16_rest(float v, float hi) { return fabsf(hi) < INFINITY ? v - hi : 0.0f; }
-__device__ __forceinline__ void split_bf16x2(float v0, float v1, uint32_t& hi, uint32_t& lo) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
-  const __nv_bfloat162 l = __floats2bfloat162_rn(bf16_rest(v0, __low2float(h)), bf16_rest(v1, __high2float(h)));
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  lo = *reinterpret_cast<const uint32_t*>(&l);
+// Two fp32 values as three pairs of bf16, cut off instead of rounded: each part takes eight bits of the significand,
+// so that their sum is the value (but for bits below the normal numbers), and the first cannot overflow.
+// An infinity or a NaN stays in the first part alone (inf - inf would make a NaN of the next).
+constexpr int kLoraParts = 3;
+__device__ __forceinline__ void split_bf16x2(float v0, float v1, uint32_t (&part)[kLoraParts]) {
+#pragma unroll
+  for (int i = 0; i < kLoraParts; ++i) {
+    const uint32_t u0 = __float_as_uint(v0), u1 = __float_as_uint(v1);
+    part[i] = __byte_perm(u0, u1, 0x7632);  // the upper halves
+    const float h0 = __uint_as_float(u0 & 0xFFFF0000u), h1 = __uint_as_float(u1 & 0xFFFF0000u);
+    v0 = fabsf(h0) < INFINITY ? v0 - h0 : 0.0f;
+    v1 = fabsf(h1) < INFINITY ? v1 - h1 : 0.0f;
+  }
 }
 
 // ---------------------------------------------------------------------------- few rows
@@ -227,8 +232,8 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRows<NT>::CTAS) lora_rows_ke
   }
   cluster_sync_all();  // every rank has read the parts; s_h is complete
 
-  // delta = h B^T.  Both bf16 halves of h go through the tensor cores, so h keeps 16 bits.
-  uint32_t hi[NS][4], lo[NS][4];
+  // delta = h B^T.  The three bf16 parts of h go through the tensor cores, so h keeps its 24 bits.
+  uint32_t hp[kLoraParts][NS][4];
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
 #pragma unroll
@@ -236,8 +241,14 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRows<NT>::CTAS) lora_rows_ke
       const int r = s * 16 + q * 4;
       const float4 v = r < RP ? *reinterpret_cast<const float4*>(s_h + (g + i * 8) * LD + r)
                               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      split_bf16x2(v.x, v.y, hi[s][i], lo[s][i]);
-      split_bf16x2(v.z, v.w, hi[s][i + 2], lo[s][i + 2]);
+      uint32_t xy[kLoraParts], zw[kLoraParts];
+      split_bf16x2(v.x, v.y, xy);
+      split_bf16x2(v.z, v.w, zw);
+#pragma unroll
+      for (int part = 0; part < kLoraParts; ++part) {
+        hp[part][s][i] = xy[part];
+        hp[part][s][i + 2] = zw[part];
+      }
     }
   }
   for (int gr = g0 + warp; gr < g1; gr += kLoraWarps) {
@@ -248,8 +259,8 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRows<NT>::CTAS) lora_rows_ke
       for (int c = 0; c < 4; ++c) d[i][c] = 0.0f;
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        mma_16816(d[i], hi[s], bv[i][s].x, bv[i][s].y);
-        mma_16816(d[i], lo[s], bv[i][s].x, bv[i][s].y);
+#pragma unroll
+        for (int part = 0; part < kLoraParts; ++part) mma_16816(d[i], hp[part][s], bv[i][s].x, bv[i][s].y);
       }
     }
     const uint4 c0 = cv[0], c1 = cv[1];
@@ -280,9 +291,9 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRows<NT>::CTAS) lora_rows_ke
 //                     few tiles more or less than SMs cost nothing; x gathered and A copied by cp.async into
 //                     128-byte-swizzled tiles, tcgen05.mma into TMEM.
 //   lora_up_kernel    out = C + h B^T, the (tile, 64 columns of N) units split the same way.  A CTA sums the parts of its
-//                     tile's h in the order of K, scales it and keeps it as two bf16 halves (hi + lo: 16 bits of
-//                     h); C and B come by cp.async, the product goes into one of two TMEM buffers while the
-//                     chunk before is added and stored.
+//                     tile's h in the order of K, scales it and keeps it in TMEM as three bf16 parts (all 24 bits),
+//                     from where the products take it; C and B come by cp.async, the product goes into one of two
+//                     TMEM buffers while the chunk before is added and stored.
 // Bound by HBM: x once, C in and out; 4096 rows, rank 64, 7168 -> 4096: down 18 us for 66 MB, up 22 for 75, with
 // the sort 50 in all.  (mma.sync took 28 us for the second product of 4096 x 4096, rank
 // 64, whose bytes take 11; parts summed once by the last CTA of a tile took 8 us, in every reader 3.)
@@ -299,10 +310,13 @@ struct LoraTile {
   static constexpr int STAGES = (CTAS == 2 ? 100 : 200) * 1024 / STAGE_BYTES;
   static constexpr int DOWN_SMEM = 1024 + STAGES * STAGE_BYTES;
   static constexpr int PART_FLOATS = kLoraTileRows * RP;
-  static constexpr int H_BYTES = KB * X_BYTES;  // one half of h
   static constexpr int B_BYTES = KB * 64 * 128;
   static constexpr int RING = RP <= 64 ? 3 : 4;  // chunks of C and B in shared memory
-  static constexpr int UP_SMEM = 1024 + 2 * H_BYTES + RING * (X_BYTES + B_BYTES);
+  static constexpr int UP_SMEM = 1024 + RING * (X_BYTES + B_BYTES);
+  // TMEM of lora_up_kernel: two products of 64 columns, then the parts of h, two bf16 a column
+  static constexpr int UP_H = 128, UP_PART = RP / 2;
+  static constexpr int UP_TMEM = UP_H + kLoraParts * UP_PART <= 256 ? 256 : 512;
+  static_assert(CTAS * UP_TMEM <= 512 && UP_H + kLoraParts * UP_PART <= UP_TMEM, "TMEM");
   static_assert(CTAS * (DOWN_SMEM + 1536) <= 227 * 1024 && CTAS * (UP_SMEM + 1536) <= 227 * 1024, "shared memory");
 };
 
@@ -321,9 +335,6 @@ __device__ __forceinline__ uint4 ld_shared_16(uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ void st_shared_8(uint32_t addr, uint32_t a, uint32_t b) {
-  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
-}
 __device__ __forceinline__ void st_shared_16(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -337,6 +348,23 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint6
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// The same with A in TMEM: lane m, two consecutive values of a row in each 32-bit column.
+__device__ __forceinline__ void mma_bf16_tmem(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 32 lanes x 4 consecutive 32-bit columns: thread t writes lane (base + t).
+__device__ __forceinline__ void tmem_st_32x32b_x4(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // Instruction descriptor: bf16 x bf16 -> f32, both operands K-major, shape M x N.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
@@ -382,13 +410,7 @@ __global__ void __launch_bounds__(kLoraThreads, LoraTile<RP>::CTAS) lora_down_ke
     s_abort = 0;
     fence_mbar_init();
   }
-  pdl_wait_prior_grid();
-  pdl_launch_dependents();
-  const int KB = (p.K + 63) / 64;
-  const long long U = static_cast<long long>(p.tiles[0]) * KB;
-  const int P = lora_down_ctas(U, KB, gridDim.x);
-  if (static_cast<int>(blockIdx.x) >= P) return;
-  const int u0 = lora_begin(blockIdx.x, P, U), n = lora_begin(blockIdx.x + 1, P, U) - u0;
+  // before the next kernel may start: its CTAs take theirs early, and wait for this kernel with it
   if (warp == 0) {
     tmem_alloc(&s_tmem, TMEM_COLS);
     tmem_relinquish();
@@ -397,6 +419,16 @@ __global__ void __launch_bounds__(kLoraThreads, LoraTile<RP>::CTAS) lora_down_ke
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
+  pdl_wait_prior_grid();
+  pdl_launch_dependents();
+  const int KB = (p.K + 63) / 64;
+  const long long U = static_cast<long long>(p.tiles[0]) * KB;
+  const int P = lora_down_ctas(U, KB, gridDim.x);
+  if (static_cast<int>(blockIdx.x) >= P) {
+    if (warp == 0) tmem_dealloc(tmem, TMEM_COLS);
+    return;
+  }
+  const int u0 = lora_begin(blockIdx.x, P, U), n = lora_begin(blockIdx.x + 1, P, U) - u0;
 
   // the loads run ahead of the products, over the tiles: their own tile, place in K and ring
   int load_tile = u0 / KB, load_kb = u0 - load_tile * KB, load_stage = 0;
@@ -523,8 +555,8 @@ template <int RP>
 __global__ void __launch_bounds__(kLoraThreads, LoraTile<RP>::CTAS) lora_up_kernel(const LoraParams p) {
   typedef LoraTile<RP> L;
   constexpr int RING = L::RING;
-  constexpr uint32_t TMEM_COLS = 128;
-  constexpr uint32_t C_RING = 2 * L::H_BYTES, B_RING = C_RING + RING * L::X_BYTES;
+  constexpr uint32_t TMEM_COLS = L::UP_TMEM;
+  constexpr uint32_t C_RING = 0, B_RING = C_RING + RING * L::X_BYTES;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t done[2];
   __shared__ uint32_t s_tmem;
@@ -643,8 +675,11 @@ __global__ void __launch_bounds__(kLoraThreads, LoraTile<RP>::CTAS) lora_up_kern
     }
     {  // h (its last product of the tile before has run: every thread has waited for it)
       const int first = lora_owner(t * KB, PU, U), last = lora_owner(t * KB + KB - 1, PU, U);
-      const float adapter_scale = p.scaling ? p.scaling[ad] : 1.0f;
-      constexpr int EACH = L::PART_FLOATS / 4 / kLoraThreads, SIDE = EACH < 8 ? EACH : 8;  // quads of a thread; at once
+      const float scale = p.scaling ? p.scaling[ad] : 1.0f;
+      // a thread's row is its lane of TMEM; its quads of ranks lie side by side, half of the row's
+      constexpr int EACH = RP / 8, SIDE = EACH < 8 ? EACH : 8;  // quads of a thread; at once
+      const int m = tid % kLoraTileRows, q0 = tid / kLoraTileRows * EACH;
+      const uint32_t to = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + L::UP_H;
 #pragma unroll 1
       for (int e = 0; e < EACH; e += SIDE) {
         float4 h[SIDE];
@@ -654,28 +689,37 @@ __global__ void __launch_bounds__(kLoraThreads, LoraTile<RP>::CTAS) lora_up_kern
         for (int c = first; c <= last; ++c) {
           const int place = first == last ? 2 * gridDim.x + t : 2 * c + (c == first ? 1 : 0);
           const float4* part = reinterpret_cast<const float4*>(p.parts + static_cast<size_t>(place) * L::PART_FLOATS) +
-                               e * kLoraThreads + tid;
+                               (q0 + e) * kLoraTileRows + m;
           float4 w[SIDE];
 #pragma unroll
-          for (int i = 0; i < SIDE; ++i) w[i] = __ldcg(part + i * kLoraThreads);
+          for (int i = 0; i < SIDE; ++i) w[i] = __ldcg(part + i * kLoraTileRows);
 #pragma unroll
           for (int i = 0; i < SIDE; ++i)
             h[i] = make_float4(h[i].x + w[i].x, h[i].y + w[i].y, h[i].z + w[i].z, h[i].w + w[i].w);
         }
 #pragma unroll
-        for (int i = 0; i < SIDE; ++i) {
-          const int at = (e + i) * kLoraThreads + tid, m = at % kLoraTileRows, r = at / kLoraTileRows * 4;
-          uint32_t hi[2], lo[2];
-          if (r >= p.R) h[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // padding, which infinities in x make NaN
-          const float scale = r < p.R ? adapter_scale : 0.0f;
-          split_bf16x2(h[i].x * scale, h[i].y * scale, hi[0], lo[0]);
-          split_bf16x2(h[i].z * scale, h[i].w * scale, hi[1], lo[1]);
-          const uint32_t dst =
-              base + (r / 64) * L::X_BYTES + m * 128 + ((((r % 64) / 8) ^ (m & 7)) << 4) + (r & 4) * 2;
-          st_shared_8(dst, hi[0], hi[1]);
-          st_shared_8(dst + L::H_BYTES, lo[0], lo[1]);
+        for (int i = 0; i < SIDE; i += 2) {
+          uint32_t out[kLoraParts][4];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const bool pads = (q0 + e + i + k) * 4 >= p.R;  // padding, which infinities in x make NaN
+            const float4 v = h[i + k];
+            uint32_t xy[kLoraParts], zw[kLoraParts];
+            split_bf16x2(pads ? 0.0f : v.x * scale, pads ? 0.0f : v.y * scale, xy);
+            split_bf16x2(pads ? 0.0f : v.z * scale, pads ? 0.0f : v.w * scale, zw);
+#pragma unroll
+            for (int part = 0; part < kLoraParts; ++part) {
+              out[part][2 * k] = xy[part];
+              out[part][2 * k + 1] = zw[part];
+            }
+          }
+#pragma unroll
+          for (int part = 0; part < kLoraParts; ++part)
+            tmem_st_32x32b_x4(to + part * L::UP_PART + 2 * (q0 + e + i), out[part]);
         }
       }
+      tmem_wait_st();
+      tc_fence_before();  // the products come after the barrier below
     }
 #pragma unroll 1
     for (int c = 0; c < nc; ++c) {
@@ -686,14 +730,15 @@ __global__ void __launch_bounds__(kLoraThreads, LoraTile<RP>::CTAS) lora_up_kern
         tc_fence_after();
         const uint32_t d = tmem + ((used + c) & 1) * 64;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int part = 0; part < kLoraParts; ++part) {
+          const uint32_t h = tmem + L::UP_H + part * L::UP_PART;
 #pragma unroll
           for (int b = 0; b < L::KB; ++b) {
-            const uint64_t adesc = smem_desc_k128_sw128(base + half * L::H_BYTES + b * L::X_BYTES);
             const uint64_t bdesc = smem_desc_k128_sw128(base + B_RING + (c % RING) * L::B_BYTES + b * (64 * 128));
 #pragma unroll
-            for (int j = 0; j < (RP < 64 ? RP / 16 : 4); ++j)
-              mma_bf16(d, adesc + 2 * j, bdesc + 2 * j, idesc_bf16_f32(kLoraTileRows, 64), half + b + j > 0 ? 1u : 0u);
+            for (int j = 0; j < (RP < 64 ? RP / 16 : 4); ++j)  // 16 values are 8 columns of h
+              mma_bf16_tmem(d, h + 32 * b + 8 * j, bdesc + 2 * j, idesc_bf16_f32(kLoraTileRows, 64),
+                            part + b + j > 0 ? 1u : 0u);
           }
         }
         mma_commit(&done[(used + c) & 1]);

@@ -60,3 +60,25 @@ def test_lora_infinite_rows_are_those_of_the_definition(fg, M, R):
         np.testing.assert_array_equal(f64(got[m]), want)
     keep = [m for m in range(M) if m not in (1, 3)]
     assert torch.equal(got[keep], clean[keep])
+
+
+@pytest.mark.parametrize("M", [6, 700])
+@pytest.mark.parametrize("R", [8, 16, 32, 64, 128])
+def test_lora_sums_between_the_products_keep_fp32(fg, M, R):
+    """Whole numbers below 2^24 throughout, so that fp32 sums are exact: C holds minus the rounded update, and what
+    is left shows every bit of A x.  Exact, up to the one rounding of the output (no tolerance)."""
+    K, N, L = 512, 136, 3
+    g = gen(R + M)
+    x = torch.randint(64, 128, (M, K), generator=g)
+    a = torch.randint(0, 16, (L, R, K), generator=g)
+    b = torch.randint(-1, 2, (L, N, R), generator=g) * (torch.rand(L, N, R, generator=g) < 8 / R)
+    ids = torch.randint(0, L, (M,), generator=g)
+    h = torch.stack([a[i] @ x[m] for m, i in enumerate(ids)])
+    delta = torch.stack([b[i] @ h[m] for m, i in enumerate(ids)])
+    most = torch.stack([b[i].abs() @ h[m] for m, i in enumerate(ids)])
+    assert h.max() > 2 ** 18 and most.max() < 2 ** 24
+    C = -delta.to(torch.bfloat16)
+    want = (C.double() + delta.double()).to(torch.bfloat16)
+    dev = [t.to(torch.bfloat16).cuda() for t in (C, x, a, b)]
+    got = fg.lora_add(*dev, ids.to(torch.int32).cuda()).cpu()
+    assert torch.equal(got, want)
