@@ -22,7 +22,6 @@ constexpr int kRouteThreads = 256;
 constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kRouteMaxK = 32;
 constexpr int kRouteMaxCluster = 8;
-constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -81,13 +80,9 @@ struct RouteKey<float> {
 };
 
 // e^(x - high), high the row's largest logit.  The difference is formed first: with the type's lowest
-// value in every place of a row, a product with log2(e) before it would overflow.  ex2.approx is within
-// 2^-22 relative; results below 2^-126 become 0.
-__device__ __forceinline__ float softmax_exp(float x, float high) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((x - high) * kLog2e));
-  return y;
-}
+// value in every place of a row, a product with log2(e) before it would overflow.  expf, not ex2 of the rounded
+// product: that would lose as many units in the last place as x lies below high, and all below 2^-126.
+__device__ __forceinline__ float softmax_exp(float x, float high) { return expf(x - high); }
 
 // Reductions over the LPR lanes that hold one row (LPR a power of two).
 template <int LPR, int N>

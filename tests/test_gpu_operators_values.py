@@ -82,3 +82,43 @@ def test_lora_sums_between_the_products_keep_fp32(fg, M, R):
     dev = [t.to(torch.bfloat16).cuda() for t in (C, x, a, b)]
     got = fg.lora_add(*dev, ids.to(torch.int32).cuda()).cpu()
     assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------------------------------- the router
+@pytest.mark.parametrize("E", [9, 60, 100, 200, 400, 1000])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_weights_far_below_the_largest_logit(fg, E, renorm):
+    """Logits in eighths, whose differences are exact: a weight is off by the roundings of e^d (2 ulp, 4 u), of the
+    sum (40 u) and of the product (2 u), however far d is below 0; below the normal numbers by half a step
+    of 2^-149 (2 ulp there: 2^-148)."""
+    g = gen(E)
+    T, k = 40, min(E, 32)
+    logits = -torch.arange(E).float()[None] * 8.25 / min(E, 13) - torch.randint(0, 8, (T, E), generator=g) / 8
+    logits[:, 3::4] -= 60.0
+    logits = (logits * 8).round() / 8
+    logits = logits.clamp(min=-104.0)
+    logits[:, 0] = 0.0
+    logits[0, 1:] = -90.125  # subnormal in every place but one
+    want = ref.route(f64(logits)[None], k, None, renorm)
+    ids, weights, _, _, _ = fg.moe_route(logits.cuda(), k, renormalize=renorm)
+    assert np.array_equal(ids.cpu().numpy(), want["ids"][0])
+    w = want["weights"][0]
+    assert np.all(np.abs(f64(weights) - w) <= 48 * U * w + 2.0 ** -147)
+
+
+@pytest.mark.parametrize("E", [9, 60, 200, 400])
+def test_route_gradient_far_below_the_largest_logit(fg, E):
+    """grad = p (h - sum p h): p carries 48 u as above, the bracket one rounding per term and sum."""
+    T, k = 17, 2
+    logits = -(torch.arange(T * E).view(T, E) % 700).float() / 8
+    logits[:, 0], logits[:, 1] = 0.0, -0.125
+    ids, weights, _, loss, slope = fg.moe_route(logits.cuda(), k)
+    want = ref.route(f64(logits)[None], k)
+    assert np.array_equal(ids.cpu().numpy(), want["ids"][0])
+    gl = torch.tensor(3.0)
+    got = f64(fg.moe_route_backward(logits.cuda(), ids, slope, None, gl.cuda()))
+    grad, _ = ref.route_backward(want, None, f64(gl)[None])
+    h = 3.0 * want["slope"][0]
+    size = want["p"][0] * (h[None] + (want["p"][0] * h).sum(1, keepdims=True))
+    # both sides' slope carries 4 u, the sum over E 40 u; below the normal numbers half steps of 2^-149
+    assert np.all(np.abs(got - grad[0]) <= 110 * U * size + 2.0 ** -146 * (1 + h.max()))
