@@ -25,10 +25,9 @@ import torch
 _HERE = pathlib.Path(__file__).resolve().parent
 LIB_PATH = _HERE / "libfp8gemm.so"
 
-for _path in (LIB_PATH, _HERE / "_operators.so"):  # the library, and the compiled part of this binding
-    if not _path.exists():
-        raise ImportError(f"{_path} is not built; run `python moe_grouped_gemm_08_b200/build.py` "
-                          "or __graft_entry__.build()")
+if not LIB_PATH.exists():
+    raise ImportError(f"{LIB_PATH} is not built; run `python moe_grouped_gemm_08_b200/build.py` "
+                      "or __graft_entry__.build()")
 
 _vp, _int = ctypes.c_void_p, ctypes.c_int
 

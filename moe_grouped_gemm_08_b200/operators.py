@@ -18,9 +18,26 @@ from __future__ import annotations
 
 import torch
 
-from . import FORMATS, FP8GemmError, _lib, _operators, _stream
+from . import FORMATS, FP8GemmError, _lib, _stream
 
-_operators.set_error(FP8GemmError)
+
+class _Missing:
+    """In the place of the compiled marshalling where it cannot be loaded: the GEMMs, which do without it, work, and
+    the operators raise."""
+
+    def __init__(self, why):
+        self.why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{name} needs {__package__}/_operators.so, which cannot be loaded ({self.why}); run "
+                          "`python moe_grouped_gemm_08_b200/build.py` or __graft_entry__.build()")
+
+
+try:
+    from . import _operators
+    _operators.set_error(FP8GemmError)
+except ImportError as e:
+    _operators = _Missing(e)
 
 
 def _there(t, stream, call, *args):
