@@ -88,10 +88,20 @@ def _build_one(so: pathlib.Path, extra, force: bool, verbose: bool) -> pathlib.P
     return so
 
 
+def binding_target() -> str:
+    """What the binding is compiled against: torch's version and place, Python's ABI."""
+    import importlib.metadata
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    return f"torch {importlib.metadata.version('torch')} at {torch}, {sysconfig.get_config_var('SOABI')}"
+
+
 def build_binding(force: bool = False) -> pathlib.Path:
-    """Compile the marshalling of the operators against the installed torch, linked to libfp8gemm.so beside it."""
+    """Compile the marshalling of the operators against the installed torch, linked to libfp8gemm.so beside it.  Built
+    again when its sources are newer, and when torch or Python is another one than it was built for."""
     src = CSRC / "operators_binding.cpp"
-    if not force and _newer(BINDING, [src, ROOT / "include" / "fp8gemm.h", pathlib.Path(__file__)]):
+    built_for, now = GEN / "operators_binding.built_for", binding_target()
+    if (not force and _newer(BINDING, [src, ROOT / "include" / "fp8gemm.h", pathlib.Path(__file__)])
+            and built_for.exists() and built_for.read_text() == now):
         return BINDING
     torch = pathlib.Path(importlib.util.find_spec("torch").submodule_search_locations[0])
     cuda = pathlib.Path(nvcc()).parent.parent if os.path.isabs(nvcc()) else pathlib.Path("/usr/local/cuda")
@@ -101,6 +111,8 @@ def build_binding(force: bool = False) -> pathlib.Path:
                            str(tmp), f"-L{HERE}", "-l:libfp8gemm.so", "-Wl,-rpath,$ORIGIN", f"-L{torch / 'lib'}",
                            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
     os.replace(tmp, BINDING)
+    GEN.mkdir(exist_ok=True)
+    built_for.write_text(now)
     return BINDING
 
 
