@@ -266,6 +266,7 @@ PyObject* moe_dispatch_fp8(PyObject* const* a) {
   if (x.dim() != 2) raise(PyExc_ValueError, "x must be [T, K]");
   const int T = to_int(x.size(0), "x"), K = to_int(x.size(1), "x");
   const Tensor& rows = rows_of(a[1], T, x);
+  const int fmt = arg_int(a[5], "fmt");
   const bool have = a[3] != Py_None;
   if (have != (a[4] != Py_None) || (!have && a[2] == Py_None)) raise(PyExc_ValueError, "give shape, or both A and sfa");
   c10::SmallVector<int64_t, 4> lead;
@@ -289,7 +290,9 @@ PyObject* moe_dispatch_fp8(PyObject* const* a) {
   const auto codes = joined(lead, {K});
   Tensor A, sfa;
   if (have) {
-    A = beside(a[3], at::kByte, codes, x, "A");
+    // codes as bytes or as values of the format, as the GEMMs take them
+    const at::ScalarType float8 = fmt == FG_E4M3 ? at::kFloat8_e4m3fn : at::kFloat8_e5m2;
+    A = beside(a[3], tensor(a[3], "A").scalar_type() == float8 ? float8 : at::kByte, codes, x, "A");
     sfa = beside(a[4], at::kFloat, scales, x, "sfa");
     apart(A, "A", &x, "x");
     apart(A, "A", &rows, "rows");
@@ -303,7 +306,7 @@ PyObject* moe_dispatch_fp8(PyObject* const* a) {
     sfa = at::zeros(scales, x.options().dtype(at::kFloat));
   }
   check(fg_moe_dispatch_fp8(ptr(x), ptr<int>(rows), ptr(A), ptr<float>(sfa), T, to_int(rows.size(1), "rows"), G, M, K,
-                            arg_int(a[5], "fmt"), stream_of(x)),
+                            fmt, stream_of(x)),
         "fg_moe_dispatch_fp8");
   return have ? tuple_of(given(a[3]), given(a[4])) : tuple_of(wrap(A), wrap(sfa));
 }

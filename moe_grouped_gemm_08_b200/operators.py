@@ -102,8 +102,8 @@ def moe_layout_masked(ids, num_experts, mmax, stream=None):
 def moe_dispatch_fp8(x, rows, shape=None, A=None, sfa=None, fmt="e4m3", stream=None):
     """Cast x bf16 [T, K] into the experts' rows: the codes and scales of cast_fp8_rows(x[t]) at every
     row of rows[t] (int32 [T, k], from moe_layout_*).  `shape`: M for the contiguous layout, (G,
-    Mmax) for the masked one; or give the outputs A uint8 [M, K] / [G, Mmax, K] and sfa.  Rows that
-    no choice has are not written.  Returns (A, sfa)."""
+    Mmax) for the masked one; or give the outputs A [M, K] / [G, Mmax, K] (uint8, or the format's float8
+    type) and sfa.  Rows that no choice has are not written.  Returns (A, sfa)."""
     if shape is not None:
         shape = (shape,) if isinstance(shape, int) else tuple(shape)
     return _call(x, stream, _operators.moe_dispatch_fp8, x, rows, shape, A, sfa, FORMATS[fmt])
