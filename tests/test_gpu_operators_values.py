@@ -84,6 +84,22 @@ def test_lora_sums_between_the_products_keep_fp32(fg, M, R):
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("M", [4, 300])
+@pytest.mark.parametrize("R", [8, 64])
+def test_lora_sums_above_the_largest_bf16_stay_finite(fg, M, R):
+    """A x = 1.9921875 2^127 + 2^119, an fp32 value that rounds to infinity in bf16; times 2^-120 it is 255.5, which is
+    256 in bf16 (a tie to even)."""
+    K, N = 32, 16
+    x, a = torch.zeros(M, K), torch.zeros(1, R, K)
+    x[:, 0], a[0, 1, 0] = 1.9921875 * 2.0 ** 64, 2.0 ** 63
+    x[:, 17], a[0, 1, 17] = 2.0 ** 60, 2.0 ** 59
+    b = torch.zeros(1, N, R)
+    b[0, :, 1] = 2.0 ** -120
+    dev = [t.to(torch.bfloat16).cuda() for t in (torch.zeros(M, N), x, a, b)]
+    out = fg.lora_add(*dev, torch.zeros(M, dtype=torch.int32, device="cuda"))
+    assert bool((out == 256.0).all())
+
+
 # ------------------------------------------------------------------------------------- the router
 @pytest.mark.parametrize("E", [9, 60, 100, 200, 400, 1000])
 @pytest.mark.parametrize("renorm", [True, False])
@@ -122,3 +138,22 @@ def test_route_gradient_far_below_the_largest_logit(fg, E):
     size = want["p"][0] * (h[None] + (want["p"][0] * h).sum(1, keepdims=True))
     # both sides' slope carries 4 u, the sum over E 40 u; below the normal numbers half steps of 2^-149
     assert np.all(np.abs(got - grad[0]) <= 110 * U * size + 2.0 ** -146 * (1 + h.max()))
+
+
+# ------------------------------------------------------------------------------------- dispatch
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_dispatch_over_all_exponents(fg, fmt):
+    """The codes and scales of the cast alone, bit for bit, for rows whose largest values run over every exponent of
+    bf16, below the normal numbers too, and whose others lie up to 2^-30 below."""
+    g = gen(5)
+    T, K = 1024, 256
+    x = torch.randn(T, K, generator=g).abs().clamp(min=2.0 ** -9) * torch.exp2(-30 * torch.rand(T, K, generator=g) ** 3)
+    x *= torch.where(torch.rand(T, K, generator=g) < 0.5, -1.0, 1.0)
+    x[:, 5::16] = -0.0
+    x = (x.double() * torch.exp2(torch.arange(T) % 262 - 136.0).double()[:, None]).clamp(-3.3e38, 3.3e38).to(torch.bfloat16).cuda()
+    rows = torch.randperm(2 * T, generator=g).view(T, 2).to(torch.int32).cuda()
+    A, sfa = fg.moe_dispatch_fp8(x, rows, shape=2 * T, fmt=fmt)
+    q, s = fg.cast_fp8_rows(x, fmt=fmt)
+    for j in range(2):
+        at = rows[:, j].long()
+        assert torch.equal(A[at], q) and torch.equal(sfa[:, at], s[:, :T])
