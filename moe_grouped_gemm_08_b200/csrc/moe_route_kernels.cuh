@@ -215,18 +215,20 @@ struct RouteParams {
 // What the sums over a sequence give.  Called by all threads of one CTA; thread e < E holds column e's
 // sum of p and count; rows: the routed tokens (same in every thread).
 __device__ __forceinline__ void route_finish(const RouteParams& p, int seq, float sum, int n, int rows, float* s_red,
-                                             unsigned long long* s_total) {
+                                             uint32_t* s_total) {
   const int e = threadIdx.x, warps = blockDim.x / 32;
-  // all choices of the sequence, T k of them, may pass 2^32: a warp sums the halves of its counts apart
+  // all choices of the sequence, T k of them, may pass 2^32: the halves of the counts are summed apart, in 32 bits each
   const uint32_t mine = e < p.E ? n : 0;
-  const unsigned long long here =
-      (static_cast<unsigned long long>(__reduce_add_sync(0xffffffffu, mine >> 16)) << 16) +
-      __reduce_add_sync(0xffffffffu, mine & 0xffffu);
-  if (e == 0) *s_total = 0;
+  const uint32_t low = __reduce_add_sync(0xffffffffu, mine & 0xffffu), high = __reduce_add_sync(0xffffffffu, mine >> 16);
+  if (e < 2) s_total[e] = 0;
   __syncthreads();
-  if ((e & 31) == 0 && here) atomicAdd(s_total, here);
+  if ((e & 31) == 0) {
+    if (low) atomicAdd(&s_total[0], low);
+    if (high) atomicAdd(&s_total[1], high);
+  }
   __syncthreads();
-  const float total = static_cast<float>(max(*s_total, 1ull)) * static_cast<float>(max(rows, 1));
+  const unsigned long long choices = (static_cast<unsigned long long>(s_total[1]) << 16) + s_total[0];
+  const float total = static_cast<float>(max(choices, 1ull)) * static_cast<float>(max(rows, 1));
   const float slope = static_cast<float>(p.E) * static_cast<float>(n) / total;
   if (e < p.E) {
     p.counts[static_cast<size_t>(seq) * p.E + e] = n;
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
   }
   if constexpr (CLUSTER) {
     __shared__ float s_red[kRouteWarps];
-    __shared__ unsigned long long s_total;
+    __shared__ uint32_t s_total[2];
     cluster_sync_all();
     if (chunk == 0) {
       static_assert(EP <= kRouteThreads, "one column per thread");
@@ -412,7 +414,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
         rows += __float_as_int(ld_dsmem_f32(mapa_shared(rows_at, c)));
       }
       cluster_sync_all();  // the parts have been read
-      route_finish(p, seq, v, n, rows, s_red, &s_total);
+      route_finish(p, seq, v, n, rows, s_red, s_total);
     } else {
       cluster_sync_all();  // no CTA leaves before its part has been read
     }
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(1024) moe_route_finish_kernel(const RouteParam
   __shared__ float s_part[1024];
   __shared__ int s_cnt[1024];
   __shared__ float s_red[32];
-  __shared__ unsigned long long s_total;
+  __shared__ uint32_t s_total[2];
   __shared__ int s_rows;
   const int seq = blockIdx.y, rank = static_cast<int>(cluster_ctarank());
   if (threadIdx.x == 0) s_rows = 0;
@@ -480,7 +482,7 @@ __global__ void __launch_bounds__(1024) moe_route_finish_kernel(const RouteParam
   cluster_sync_all();  // the parts have been read
   if (rank != 0) return;
   // columns past E (and threads of other parts) hold nothing
-  route_finish(p, seq, sum, threadIdx.x < p.E ? n : 0, rows, s_red, &s_total);
+  route_finish(p, seq, sum, threadIdx.x < p.E ? n : 0, rows, s_red, s_total);
 }
 
 struct RouteGradParams {
