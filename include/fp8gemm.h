@@ -261,7 +261,8 @@ fg_status fg_moe_route(const void* logits, int dtype, const unsigned char* mask,
 
 /* Gradient of the router: grad_logits [S][T][E] (type of the logits, rounded once from fp32) from
  * grad_weights [S][T][k] and grad_loss [S], either NULL for none, with the ids and slope of the
- * forward call with the same logits.  Tokens that were not routed (all ids -1) get zeros. */
+ * forward call with the same logits (an expert stands at most once among a token's ids; with more the
+ * order of their fp32 sum is open).  Tokens that were not routed (all ids -1) get zeros. */
 fg_status fg_moe_route_backward(const void* logits, int dtype, const int* ids, const float* slope,
                                 const float* grad_weights, const float* grad_loss, void* grad_logits, int S,
                                 int T, int E, int k, int renormalize, void* stream);

@@ -62,7 +62,7 @@ __device__ __forceinline__ void split_bf16x2(float v0, float v1, uint32_t (&part
 // cluster takes a CL-th of K for h = A x (its warps strided over 32-wide blocks), the parts are
 // summed through distributed shared memory in rank order, and each rank then takes a CL-th of N.
 // Bound by latency: the loads of a phase are all asked for before the first is used, and the first columns of
-// B and C before h is ready.  K 7168, N 4096, rank 16: one row 3.9 us, 64 rows of 64 adapters 8.7, 128 rows 12.
+// B and C before h is ready.  K 7168, N 4096, rank 16: one row 4.6 us, 64 rows of 64 adapters 8.9, 128 rows 12.
 // NT: eights of the rank held (R <= 8 NT).
 template <int NT>
 struct LoraRows {
@@ -294,9 +294,10 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRows<NT>::CTAS) lora_rows_ke
 //                     tile's h in the order of K, scales it and keeps it in TMEM as three bf16 parts (all 24 bits),
 //                     from where the products take it; C and B come by cp.async, the product goes into one of two
 //                     TMEM buffers while the chunk before is added and stored.
-// Bound by HBM: x once, C in and out; 4096 rows, rank 64, 7168 -> 4096: down 18 us for 66 MB, up 22 for 75, with
-// the sort 50 in all.  (mma.sync took 28 us for the second product of 4096 x 4096, rank
-// 64, whose bytes take 11; parts summed once by the last CTA of a tile took 8 us, in every reader 3.)
+// Bound by HBM: x once, C in and out; 4096 rows, rank 64, 7168 -> 4096: 52 us with the sort (one at a
+// time, from cold caches: down 18.6 us for 66 MB, up 28 for 75).  mma.sync took 28 us for the second product of 4096 x
+// 4096, rank 64, whose bytes take 11; parts summed once by the last CTA of a tile took 8 us, in every reader 3; h as two
+// parts in shared memory, so 16 bits of it, 51 us in all.
 constexpr int kLoraTileRows = 128;
 constexpr uint64_t kLoraWaitNs = 2000000000ull;  // far above any legal wait
 constexpr int kLoraTimeout = 6;                  // FG_ERR_TIMEOUT

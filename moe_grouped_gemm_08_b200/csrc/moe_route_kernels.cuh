@@ -246,8 +246,8 @@ __device__ __forceinline__ void route_finish(const RouteParams& p, int seq, floa
 // Forward, one CTA per (chunk of rows, sequence).  LPR lanes hold a row, NPL values each, so a warp
 // works on 32 / LPR rows at once; the next rows are loaded while the present ones are worked on.  Each
 // lane sorts its keys once (a network in registers), then every choice is one reduction over the heads of
-// the lanes' lists and a shift in the winner's.  Bound by the integer pipe, about 470 instructions per row of
-// 256: 32768 rows in 8 sequences, bf16, top 8, in 24 us with the finishing kernel (17 MB, which take 2.6).
+// the lanes' lists and a shift in the winner's.  Bound by the integer pipe, about 510 instructions per row of
+// 256: 32768 rows in 8 sequences, bf16, top 8, in 26 us with the finishing kernel (17 MB, which take 2.6).
 // CLUSTER: the sequence's CTAs are one cluster, whose first CTA sums the others' parts over distributed
 // shared memory and finishes; otherwise the parts go to memory for moe_route_finish_kernel.
 template <typename T, int LPR, int NPL, int V, bool CLUSTER>
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
 // Sums of the chunks of one sequence in a fixed order, then its counts, slopes and loss.  A cluster of
 // kFinishCluster CTAs of 1024 threads: each takes as many parts of the chunks side by side as columns leave room
 // for, and the first sums the CTAs' parts over distributed shared memory (the router of 32768 rows of 256 in one
-// sequence, 586 chunks: 30 us, 39 us with one CTA here; now 1024 chunks and 27 us).
+// sequence: 29 us; at 586 chunks one CTA here took 9 us more than eight).
 constexpr int kFinishCluster = 8;
 __global__ void __launch_bounds__(1024) moe_route_finish_kernel(const RouteParams p) {
   __shared__ float s_part[1024];
@@ -500,7 +500,7 @@ struct RouteGradParams {
 //   renormalised:      d l_e = p_e (h_e - sum u h / sum u)  (+ w_j (g_j - sum_j w g) at the choices),
 // w the softmax over the chosen logits.  All four sums are reduced together.  Rows without a choice get
 // zeros.  What the choices add goes through a row of shared memory, which is zero between rows.  32768 rows of
-// 256, bf16, top 8: 13.4 us for 36 MB, bound by instructions (about 300 a row).
+// 256, bf16, top 8: 15.8 us for 36 MB, bound by instructions (about 350 a row).
 template <typename T, int LPR, int NPL, int V>
 __global__ void __launch_bounds__(kRouteThreads) moe_route_backward_kernel(const RouteGradParams p) {
   constexpr int RPW = 32 / LPR;

@@ -40,7 +40,8 @@ int sm_count() {
 }
 
 // Programmatic dependent launch, as the GEMMs are launched: every kernel here waits for the preceding
-// grid before it touches global memory, and only then lets the next one start.
+// grid before it lets the next one start, and before it touches global memory.  lora_up_kernel alone reads earlier
+// what the grid before it, which has waited for all others, does not write.
 template <typename... Params, typename... Args>
 fg_status launch(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, void* stream, int cluster,
                  const Args&... args) {
@@ -119,7 +120,7 @@ int route_step(int E) { return fg::kRouteWarps * (E <= 64 ? 4 : E <= 128 ? 2 : 1
 // How a sequence of T rows is split over CTAs.  Up to four rows a warp of eight CTAs: one cluster per
 // sequence, which also finishes (one launch).  Otherwise a second kernel finishes, and the chunks are such that
 // every SM gets about eight CTAs where that leaves them three rows a warp, else four (32768 rows of 256
-// experts: 26.8 us with eight, 29.2 with four; 8192 rows: 15.7 and 13.3, as the chunks have to be summed).
+// experts: 28.9 us with eight, 31.7 with four; 8192 rows: 16.3 and 14.1, as the chunks have to be summed).
 struct RouteSplit {
   int rows, chunks;  // rows per CTA, CTAs per sequence
   bool cluster;
@@ -275,8 +276,10 @@ fg_status lora_rows_launch(const fg::LoraParams& p, void* stream) {
   return launch(fg::lora_rows_kernel<NT, CL>, dim3(static_cast<unsigned>(p.M) * CL), fg::kLoraThreads, smem, stream, CL, p);
 }
 
-// Eight CTAs a cluster while all clusters are resident at once (rank 16: 64 rows 8.8 us, with four 10.7),
-// else four (128 rows of 64 adapters 12.1 us, with eight 14.4).
+// Eight CTAs a cluster up to 64 rows, else four.  With eight, then four, K 7168, N 4096: 64 rows of 64 adapters 8.9 and
+// 11.3 us at rank 16 (31.1 and 23.0 at rank 64, 60.8 and 57.2 at rank 128, where fewer CTAs fit at once), of 8
+// adapters 6.9 and 8.4, 13.5 and 16.0, 17.8 and 23.9; 128 rows of 64 adapters 15.0 and 12.5, 34.7 and 24.9,
+// 83.5 and 61.7, of 8 adapters 7.7 and 8.6, 14.8 and 17.4, 26.4 and 26.9.
 template <int NT>
 fg_status lora_rows_pick(const fg::LoraParams& p, void* stream) {
   return p.M <= 64 ? lora_rows_launch<NT, 8>(p, stream) : lora_rows_launch<NT, 4>(p, stream);
@@ -293,9 +296,12 @@ fg_status lora_tiles_launch(const fg::LoraParams& p, int sms, void* stream) {
   return launch(fg::lora_up_kernel<RP>, grid, fg::kLoraThreads, L::UP_SMEM, stream, 1, p);
 }
 
-// Many rows: tiles of 128 rows, sorted by adapter (300 rows of 4 adapters, rank 64: 22 us either way).  Few, or more
-// adapters than the sort takes: groups of 16, which the kernel finds by reading all rows' adapters, so that
-// its time grows with the square of the rows (hence kMostUnsortedRows).
+// Many rows: tiles of 128 rows, sorted by adapter.  Few, or more adapters than the sort takes: groups of 16, which the
+// kernel finds by reading all rows' adapters, so that its time grows with the square of the rows (hence
+// kMostUnsortedRows).  Tiles, then groups, K 7168, N 4096: 300 rows of 8 adapters 19.2 and 12.0 us at rank 16, 25.2 and
+// 21.5 at rank 64, 36.2 and 36.6 at rank 128; 512 rows 19.5 and 14.7, 24.9 and 27.9, 36.9 and 55.9; 1000 rows 23.4
+// and 25.2, 32.6 and 45.9, 41.9 and 90.2.  (Of 64 adapters, half empty tiles: 300 rows 45 and 15, 55 and 35, 93 and 83;
+// 1000 rows 47 and 29, 56 and 57, 96 and 119.)
 bool lora_by_tiles(int M, int L) { return L > 0 && L < FG_MOE_MAX_EXPERTS && M > 256; }
 constexpr int kMostUnsortedRows = 1 << 18;
 
