@@ -88,11 +88,15 @@ def _build_one(so: pathlib.Path, extra, force: bool, verbose: bool) -> pathlib.P
     return so
 
 
+def torch_version() -> str:
+    import torch
+    return str(torch.__version__)
+
+
 def binding_target() -> str:
     """What the binding is compiled against: torch's version and place, Python's ABI."""
-    import importlib.metadata
     torch = importlib.util.find_spec("torch").submodule_search_locations[0]
-    return f"torch {importlib.metadata.version('torch')} at {torch}, {sysconfig.get_config_var('SOABI')}"
+    return f"torch {torch_version()} at {torch}, {sysconfig.get_config_var('SOABI')}"
 
 
 def build_binding(force: bool = False) -> pathlib.Path:
@@ -107,7 +111,8 @@ def build_binding(force: bool = False) -> pathlib.Path:
     cuda = pathlib.Path(nvcc()).parent.parent if os.path.isabs(nvcc()) else pathlib.Path("/usr/local/cuda")
     includes = [ROOT / "include", sysconfig.get_paths()["include"], torch / "include", cuda / "include"]
     tmp = BINDING.with_suffix(".so.tmp%d" % os.getpid())
-    subprocess.check_call(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", *(f"-I{i}" for i in includes), str(src), "-o",
+    subprocess.check_call(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f'-DFG_TORCH_VERSION="{torch_version()}"',
+                           *(f"-I{i}" for i in includes), str(src), "-o",
                            str(tmp), f"-L{HERE}", "-l:libfp8gemm.so", "-Wl,-rpath,$ORIGIN", f"-L{torch / 'lib'}",
                            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
     os.replace(tmp, BINDING)

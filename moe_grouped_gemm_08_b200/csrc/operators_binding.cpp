@@ -442,4 +442,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_operators", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__operators() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__operators() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", FG_TORCH_VERSION) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -35,6 +35,9 @@ class _Missing:
 
 try:
     from . import _operators
+    _built_for = getattr(_operators, "torch_version", "another")
+    if _built_for != torch.__version__:
+        raise ImportError(f"built for torch {_built_for}, this is {torch.__version__}")
     _operators.set_error(FP8GemmError)
 except ImportError as e:
     _operators = _Missing(e)

@@ -29,7 +29,7 @@ def test_binding_is_built_again_for_another_torch(build, monkeypatch):
     build.build_binding()
     build.build_binding()
     assert len(build.runs) == 1  # nothing changed
-    monkeypatch.setattr("importlib.metadata.version", lambda name: "99.0")
+    monkeypatch.setattr(build, "torch_version", lambda: "99.0")
     build.build_binding()
     assert len(build.runs) == 2
     build.build_binding()

@@ -13,6 +13,7 @@ import moe_grouped_gemm_08_b200 as fg
 
 SCRIPT = """
 import torch
+{before}
 import moe_grouped_gemm_08_b200 as fg
 assert fg.LIB_PATH.parent.parent.samefile({where!r}), fg.LIB_PATH
 assert fg.lib.fp8_gemm_nt(None, None, None, None, None, 1, 8, 16, None) == 1
@@ -36,10 +37,18 @@ def copied(tmp_path):
     return to
 
 
+def run(where, before=""):
+    subprocess.run([sys.executable, "-c", SCRIPT.format(where=str(where), before=before)], cwd=where, check=True,
+                   env={"PATH": "/usr/bin:/bin", "PYTHONPATH": str(where)})
+
+
 @pytest.mark.parametrize("broken", [False, True])
 def test_gemms_work_without_the_operators_binding(tmp_path, broken):
     to = copied(tmp_path)
     if broken:  # one that the loader refuses
         (to / "_operators.so").write_bytes(b"not a library")
-    subprocess.run([sys.executable, "-c", SCRIPT.format(where=str(tmp_path))], cwd=tmp_path, check=True,
-                   env={"PATH": "/usr/bin:/bin", "PYTHONPATH": str(tmp_path)})
+    run(tmp_path)
+
+
+def test_a_binding_built_for_another_torch_is_not_used():
+    run(pathlib.Path(fg.__file__).parent.parent, 'torch.__version__ = "1.99.0+cu999"')
