@@ -140,6 +140,24 @@ def test_route_gradient_far_below_the_largest_logit(fg, E):
     assert np.all(np.abs(got - grad[0]) <= 110 * U * size + 2.0 ** -146 * (1 + h.max()))
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("T,E", [(40, 60), (5000, 256)])
+def test_route_one_bad_logit_shows_in_its_sequence_alone(fg, T, E, bad):
+    g = gen(T)
+    logits = torch.randn(3, T, E, generator=g)
+    clean = fg.moe_route(logits.cuda(), 3)
+    want = fg.moe_route_backward(logits.cuda(), clean[0], clean[4], clean[1], torch.ones(3, device="cuda"))
+    logits[1, 7, 11] = bad
+    ids, weights, counts, loss, slope = fg.moe_route(logits.cuda(), 3)
+    assert torch.isnan(loss).tolist() == [False, True, False]
+    assert int(ids[1, 7, 0] == 11) == (bad == float("inf")) and len(set(ids[1, 7].tolist())) == 3
+    got = fg.moe_route_backward(logits.cuda(), ids, slope, weights, torch.ones(3, device="cuda"))
+    assert bool(got[1, 7].isnan().all()) and int(got.isnan().sum()) == E
+    for s in (0, 2):
+        assert torch.equal(ids[s], clean[0][s]) and torch.equal(got[s], want[s]) and torch.equal(loss[s], clean[3][s])
+    assert torch.equal(weights[1, :7], clean[1][1, :7]) and torch.equal(weights[1, 8:], clean[1][1, 8:])
+
+
 # ------------------------------------------------------------------------------------- dispatch
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
 def test_dispatch_over_all_exponents(fg, fmt):
